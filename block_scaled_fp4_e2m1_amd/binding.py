@@ -46,6 +46,32 @@ class MoeEpilogueArgs(ctypes.Structure):
     ]
 
 
+class BlockNormArgs(ctypes.Structure):
+    _fields_ = [
+        ("x", _c_ptr),
+        ("residual", _c_ptr),
+        ("w_post", _c_ptr),
+        ("w_pre", _c_ptr),
+        ("gate", _c_ptr),
+        ("scale", ctypes.c_double),
+        ("eps", ctypes.c_double),
+        ("T", _c_i64),
+        ("H", _c_i64),
+        ("groups", _c_i64),
+        ("res_out", _c_ptr),
+        ("z", _c_ptr),
+        ("q", _c_ptr),
+        ("s", _c_ptr),
+        ("dres_out", _c_ptr),
+        ("dz", _c_ptr),
+        ("dx", _c_ptr),
+        ("dres", _c_ptr),
+        ("dw_post", _c_ptr),
+        ("dw_pre", _c_ptr),
+        ("dgate", _c_ptr),
+    ]
+
+
 # name -> (restype, argtypes)
 _SIGNATURES = {
     "bsfp4_version": (ctypes.c_int, []),
@@ -55,6 +81,25 @@ _SIGNATURES = {
     "fp4_global_scale": (ctypes.c_int, [_c_ptr, _c_i64, _c_ptr, _c_ptr, _c_size, _c_ptr]),
     "fp4_quantize": (ctypes.c_int, [ctypes.c_int, _c_ptr, _c_i64, _c_i64, _c_ptr, _c_ptr, _c_i64,
                                     _c_ptr, _c_ptr, _c_ptr]),
+    "bsfp4_int8_quantize": (ctypes.c_int, [_c_ptr, _c_i64, _c_i64, _c_ptr, _c_ptr, _c_ptr]),
+    "bsfp4_int8_gemm_workspace_size": (_c_size, [_c_i64, _c_i64, _c_i64]),
+    "bsfp4_int8_gemm": (ctypes.c_int, [_c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_i64,
+                                       _c_ptr, _c_size, _c_ptr]),
+    "bsfp4_int8_quantize_gemm_workspace_size": (_c_size, [_c_i64, _c_i64, _c_i64]),
+    "bsfp4_int8_quantize_gemm": (ctypes.c_int, [_c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_i64,
+                                                _c_ptr, _c_size, _c_ptr]),
+    "bsfp4_int8_gated_ffn_workspace_size": (_c_size, [_c_i64, _c_i64, _c_i64]),
+    "bsfp4_int8_gated_ffn": (ctypes.c_int, [_c_ptr, _c_ptr, _c_ptr, _c_ptr, ctypes.c_int, _c_ptr, _c_i64, _c_i64,
+                                            _c_i64, _c_ptr, _c_size, _c_ptr]),
+    "bsfp4_gated_ffn_workspace_size": (_c_size, [_c_i64, _c_i64, _c_i64]),
+    "bsfp4_gated_ffn": (ctypes.c_int, [_c_ptr, _c_ptr, ctypes.c_int, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_i64,
+                                       _c_ptr, _c_size, _c_ptr]),
+    "bsfp4_gated_ffn_backward_workspace_size": (_c_size, [_c_i64, _c_i64, _c_i64]),
+    "bsfp4_gated_ffn_backward": (ctypes.c_int, [_c_ptr, _c_ptr, _c_ptr, _c_ptr, ctypes.c_int, _c_ptr, _c_ptr,
+                                                _c_i64, _c_i64, _c_i64, _c_ptr, _c_size, _c_ptr]),
+    "bsfp4_block_norm": (ctypes.c_int, [ctypes.POINTER(BlockNormArgs), _c_ptr]),
+    "bsfp4_block_norm_backward_workspace_size": (_c_size, [_c_i64, _c_i64, _c_i64]),
+    "bsfp4_block_norm_backward": (ctypes.c_int, [ctypes.POINTER(BlockNormArgs), _c_ptr, _c_size, _c_ptr]),
     "fp4_gemm_workspace_size": (_c_size, [ctypes.c_int, _c_i64, _c_i64, _c_i64]),
     "fp4_gemm": (ctypes.c_int, [ctypes.c_int, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr,
                                 _c_i64, _c_i64, _c_i64, _c_ptr, _c_size, _c_ptr]),
@@ -351,6 +396,290 @@ def w4a16_gemm(A, B, SFB, alpha: torch.Tensor | None = None,
     _check(lib.w4a16_gemm(_p(A), _p(B), _p(SFB), _p(alpha), _p(D), M, N, K, _p(ws),
                           0 if ws is None else ws.numel(), _stream(A.device)), "w4a16_gemm")
     return D
+
+
+# ---- 8-bit integers, the gated feed-forward product, block norms
+
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+
+
+def _act(act) -> int:
+    try:
+        return ACTIVATIONS[act]
+    except (KeyError, TypeError):
+        raise ValueError(f"unknown activation {act!r} (one of {', '.join(ACTIVATIONS)})") from None
+
+
+def _out(t, shape, dtype, name):
+    if t is not None:
+        _need(t, dtype, name)
+        _shape(t, shape, name)
+
+
+def _multiple(v, step, name):
+    if v % step:
+        raise ValueError(f"{name}={v} is not a multiple of {step}")
+
+
+def _call(dev, what, fn, args, ws_bytes):
+    """fn(*args, ws, ws_bytes, stream) on the tensors' device and its current stream."""
+    with torch.cuda.device(dev):
+        ws = _workspace(ws_bytes, dev)
+        _check(fn(*args, _p(ws), ws_bytes, _stream(dev)), what)
+
+
+def int8_quantize(x: torch.Tensor, q: torch.Tensor | None = None, s: torch.Tensor | None = None):
+    """bf16 [M, K] -> (8-bit rows int8 [M, K], scales float32 [M]), x ~ q * s per row (token):
+    s = max|x| / 127, q = round-to-even(127 x / max|x|)."""
+    _need(x, torch.bfloat16, "x")
+    _dims(x, 2, "x")
+    M, K = x.shape
+    _multiple(K, 8, "K")
+    _out(q, (M, K), torch.int8, "q")
+    _out(s, (M,), torch.float32, "s")
+    dev = _device((x, "x"), (q, "q"), (s, "s"))
+    if q is None:
+        q = torch.empty((M, K), dtype=torch.int8, device=dev)
+    if s is None:
+        s = torch.empty(M, dtype=torch.float32, device=dev)
+    with torch.cuda.device(dev):
+        _check(load().bsfp4_int8_quantize(_p(x), M, K, _p(q), _p(s), _stream(dev)), "bsfp4_int8_quantize")
+    return q, s
+
+
+def _int8_weight(B, SB, K, name, sname):
+    _need(B, torch.int8, name)
+    _need(SB, torch.float32, sname)
+    _dims(B, 2, name)
+    if B.shape[1] != K:
+        raise ValueError(f"the activations have K={K} but {name} has K={B.shape[1]}")
+    _multiple(K, 16, "K")
+    _shape(SB, (B.shape[0],), sname)
+
+
+def _int8_bias(bias, N):
+    if bias is not None:
+        _need(bias, torch.bfloat16, "bias")
+        _shape(bias, (N,), "bias")
+
+
+def int8_gemm(A, SA, B, SB, bias: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """D = bf16((A @ B^T) * SA[:, None] * SB + bias); A int8 [M, K], SA [M], B int8 [N, K], SB [N]."""
+    _need(A, torch.int8, "A")
+    _need(SA, torch.float32, "SA")
+    _dims(A, 2, "A")
+    M, K = A.shape
+    _int8_weight(B, SB, K, "B", "SB")
+    N = B.shape[0]
+    _multiple(N, 8, "N")
+    _shape(SA, (M,), "SA")
+    _int8_bias(bias, N)
+    _out(out, (M, N), torch.bfloat16, "out")
+    dev = _device((A, "A"), (SA, "SA"), (B, "B"), (SB, "SB"), (bias, "bias"), (out, "out"))
+    D = out if out is not None else torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    lib = load()
+    _call(dev, "bsfp4_int8_gemm", lib.bsfp4_int8_gemm,
+          (_p(A), _p(SA), _p(B), _p(SB), _p(bias), _p(D), M, N, K), lib.bsfp4_int8_gemm_workspace_size(M, N, K))
+    return D
+
+
+def int8_quantize_gemm(x, B, SB, bias: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """D = int8_gemm(*int8_quantize(x), B, SB, bias) in one call; x bf16 [M, K]."""
+    _need(x, torch.bfloat16, "x")
+    _dims(x, 2, "x")
+    M, K = x.shape
+    _int8_weight(B, SB, K, "B", "SB")
+    N = B.shape[0]
+    _multiple(N, 8, "N")
+    _int8_bias(bias, N)
+    _out(out, (M, N), torch.bfloat16, "out")
+    dev = _device((x, "x"), (B, "B"), (SB, "SB"), (bias, "bias"), (out, "out"))
+    D = out if out is not None else torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    lib = load()
+    _call(dev, "bsfp4_int8_quantize_gemm", lib.bsfp4_int8_quantize_gemm,
+          (_p(x), _p(B), _p(SB), _p(bias), _p(D), M, N, K), lib.bsfp4_int8_quantize_gemm_workspace_size(M, N, K))
+    return D
+
+
+def _gated_rows(W13, name="W13") -> int:
+    if W13.shape[0] % 2:
+        raise ValueError(f"{name} must hold gate rows and as many up rows, got {W13.shape[0]} rows")
+    I = W13.shape[0] // 2
+    _multiple(I, 8, "I")
+    return I
+
+
+def int8_gated_ffn(A, SA, W13, SW13, act="silu", out: torch.Tensor | None = None) -> torch.Tensor:
+    """h = bf16(act(G) * U), [G | U] = (A @ W13^T) * SA[:, None] * SW13; A int8 [M, K], W13 int8 [2 I, K]
+    (gate rows, then up rows)."""
+    a = _act(act)
+    _need(A, torch.int8, "A")
+    _need(SA, torch.float32, "SA")
+    _dims(A, 2, "A")
+    M, K = A.shape
+    _int8_weight(W13, SW13, K, "W13", "SW13")
+    I = _gated_rows(W13)
+    _shape(SA, (M,), "SA")
+    _out(out, (M, I), torch.bfloat16, "out")
+    dev = _device((A, "A"), (SA, "SA"), (W13, "W13"), (SW13, "SW13"), (out, "out"))
+    h = out if out is not None else torch.empty((M, I), dtype=torch.bfloat16, device=dev)
+    lib = load()
+    _call(dev, "bsfp4_int8_gated_ffn", lib.bsfp4_int8_gated_ffn,
+          (_p(A), _p(SA), _p(W13), _p(SW13), a, _p(h), M, I, K), lib.bsfp4_int8_gated_ffn_workspace_size(M, I, K))
+    return h
+
+
+def _gated_args(x, W13):
+    _need(x, torch.bfloat16, "x")
+    _need(W13, torch.bfloat16, "W13")
+    _dims(x, 2, "x")
+    _dims(W13, 2, "W13")
+    M, H = x.shape
+    if W13.shape[1] != H:
+        raise ValueError(f"x has H={H} but W13 has H={W13.shape[1]}")
+    _multiple(H, 8, "H")
+    return M, H, _gated_rows(W13)
+
+
+def gated_ffn(x, W13, act="silu", save_gate_up: bool = False, out: torch.Tensor | None = None):
+    """h = bf16(act(G) * U), [G | U] = x @ W13^T; x bf16 [M, H], W13 bf16 [2 I, H] (gate rows, then up rows).
+    With save_gate_up returns (h, bf16 [G | U]) for gated_ffn_backward."""
+    a = _act(act)
+    M, H, I = _gated_args(x, W13)
+    _out(out, (M, I), torch.bfloat16, "out")
+    dev = _device((x, "x"), (W13, "W13"), (out, "out"))
+    h = out if out is not None else torch.empty((M, I), dtype=torch.bfloat16, device=dev)
+    gate_up = torch.empty((M, 2 * I), dtype=torch.bfloat16, device=dev) if save_gate_up else None
+    lib = load()
+    _call(dev, "bsfp4_gated_ffn", lib.bsfp4_gated_ffn, (_p(x), _p(W13), a, _p(h), _p(gate_up), M, I, H),
+          lib.bsfp4_gated_ffn_workspace_size(M, I, H))
+    return (h, gate_up) if save_gate_up else h
+
+
+def gated_ffn_backward(dh, x, W13, gate_up, act="silu", need_dx: bool = True, need_dW13: bool = True):
+    """Gradients (dx [M, H], dW13 [2 I, H]) of gated_ffn from dh [M, I] and the saved gate_up [M, 2 I], all
+    bf16; None for one that is not needed."""
+    a = _act(act)
+    M, H, I = _gated_args(x, W13)
+    _need(dh, torch.bfloat16, "dh")
+    _shape(dh, (M, I), "dh")
+    _need(gate_up, torch.bfloat16, "gate_up")
+    _shape(gate_up, (M, 2 * I), "gate_up")
+    dev = _device((dh, "dh"), (x, "x"), (W13, "W13"), (gate_up, "gate_up"))
+    dx = torch.empty((M, H), dtype=torch.bfloat16, device=dev) if need_dx else None
+    dW = torch.empty((2 * I, H), dtype=torch.bfloat16, device=dev) if need_dW13 else None
+    if dx is None and dW is None:
+        return None, None
+    lib = load()
+    _call(dev, "bsfp4_gated_ffn_backward", lib.bsfp4_gated_ffn_backward,
+          (_p(dh), _p(x), _p(W13), _p(gate_up), a, _p(dx), _p(dW), M, I, H),
+          lib.bsfp4_gated_ffn_backward_workspace_size(M, I, H))
+    return dx, dW
+
+
+def _norm_args(x, rows, rows_name, w_post, w_pre, gate, scale, eps) -> BlockNormArgs:
+    """Checks what forward and backward share; `rows` is the [T, H] tensor that is always there."""
+    _need(rows, torch.bfloat16, rows_name)
+    _dims(rows, 2, rows_name)
+    T, H = rows.shape
+    _multiple(H, 8, "H")
+    groups = 1
+    if x is not None:
+        _need(x, torch.bfloat16, "x")
+        _shape(x, (T, H), "x")
+    elif w_post is not None or gate is not None:
+        raise ValueError("without x there is no w_post and no gate")
+    elif w_pre is None:
+        raise ValueError("neither x nor w_pre is given")
+    for w, n in ((w_post, "w_post"), (w_pre, "w_pre")):
+        if w is not None:
+            _need(w, torch.bfloat16, n)
+            _shape(w, (H,), n)
+    if gate is not None:
+        _need(gate, torch.bfloat16, "gate")
+        if gate.dim() not in (1, 2) or gate.shape[-1] != H:
+            raise ValueError(f"gate must have shape ({H},) or (groups, {H}), got {tuple(gate.shape)}")
+        groups = 1 if gate.dim() == 1 else gate.shape[0]
+        if groups == 0 or T % groups:
+            raise ValueError(f"the {T} rows are not a multiple of the {groups} gate rows")
+    if not 0.0 < eps < 1e30:
+        raise ValueError(f"eps must be positive and finite, got {eps}")
+    return BlockNormArgs(scale=scale, eps=eps, T=T, H=H, groups=groups)
+
+
+def _fill(a: BlockNormArgs, **tensors):
+    for name, t in tensors.items():
+        if t is not None:
+            setattr(a, name, t.data_ptr())
+
+
+def block_norm(x, residual, w_post=None, w_pre=None, gate=None, scale: float = 1.0, eps: float = 1e-6,
+               fmt: str = "bf16", res_out: torch.Tensor | None = None):
+    """The norms around a block, with its gate and residual add:
+
+        res = bf16(residual + (gate * scale) * rms_norm(x, w_post));  z = rms_norm(res, w_pre)
+
+    x, residual bf16 [T, H]; w_post, w_pre bf16 [H]; gate bf16 [H] or [groups, H] (T / groups consecutive
+    rows each).  Without w_post x is added as it is; without x only z = rms_norm(residual, w_pre) is computed
+    and res is residual itself.  Returns (res, z), (res, q, s) for fmt="int8" (z quantised per token as by
+    int8_quantize) or res alone without w_pre.  res_out may be residual (in place)."""
+    if fmt not in ("bf16", "int8"):
+        raise ValueError(f"unknown output format {fmt!r} (bf16 or int8)")
+    a = _norm_args(x, residual, "residual", w_post, w_pre, gate, scale, eps)
+    T, H = residual.shape
+    if fmt == "int8":
+        if w_pre is None:
+            raise ValueError("fmt='int8' needs w_pre")
+    if res_out is not None and x is None:
+        raise ValueError("without x nothing is written to res_out")
+    _out(res_out, (T, H), torch.bfloat16, "res_out")
+    dev = _device((residual, "residual"), (x, "x"), (w_post, "w_post"), (w_pre, "w_pre"), (gate, "gate"),
+                  (res_out, "res_out"))
+    res = residual
+    if x is not None:
+        res = res_out if res_out is not None else torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        _fill(a, res_out=res)
+    outs = ()
+    if w_pre is not None and fmt == "bf16":
+        outs = (torch.empty((T, H), dtype=torch.bfloat16, device=dev),)
+        _fill(a, z=outs[0])
+    elif w_pre is not None:
+        outs = (torch.empty((T, H), dtype=torch.int8, device=dev), torch.empty(T, dtype=torch.float32, device=dev))
+        _fill(a, q=outs[0], s=outs[1])
+    _fill(a, x=x, residual=residual, w_post=w_post, w_pre=w_pre, gate=gate)
+    with torch.cuda.device(dev):
+        _check(load().bsfp4_block_norm(ctypes.byref(a), _stream(dev)), "bsfp4_block_norm")
+    return (res, *outs) if outs else res
+
+
+def block_norm_backward(dres, dz, x, res, w_post=None, w_pre=None, gate=None, scale: float = 1.0,
+                        eps: float = 1e-6):
+    """Gradients of block_norm (fmt="bf16"): dres and dz bf16 [T, H] are those of its outputs (dres None:
+    zeros; dz None without w_pre), res its first output.  Returns (dx, dresidual, dw_post, dw_pre, dgate), bf16 for the
+    rows, float32 for the vectors, None for those that were not given."""
+    rows = res if res is not None else dres
+    a = _norm_args(x, rows, "res" if res is not None else "dres", w_post, w_pre, gate, scale, eps)
+    T, H = rows.shape
+    if w_pre is not None and (res is None or dz is None):
+        raise ValueError("w_pre needs res and dz")
+    if w_pre is None and dz is not None:
+        raise ValueError("dz without w_pre")
+    if w_pre is None and dres is None:
+        raise ValueError("without w_pre dres is needed")
+    for t, n in ((dres, "dres"), (dz, "dz")):
+        _out(t, (T, H), torch.bfloat16, n)
+    dev = _device((rows, "res"), (dres, "dres"), (dz, "dz"), (x, "x"), (w_post, "w_post"), (w_pre, "w_pre"),
+                  (gate, "gate"))
+    row = lambda: torch.empty((T, H), dtype=torch.bfloat16, device=dev)  # noqa: E731
+    vec = lambda w: None if w is None else torch.empty(w.shape, dtype=torch.float32, device=dev)  # noqa: E731
+    dx, dresidual = (row() if x is not None else None), row()
+    dw_post, dw_pre, dgate = vec(w_post), vec(w_pre), vec(gate)
+    _fill(a, x=x, w_post=w_post, w_pre=w_pre, gate=gate, res_out=res, dres_out=dres, dz=dz, dx=dx, dres=dresidual,
+          dw_post=dw_post, dw_pre=dw_pre, dgate=dgate)
+    lib = load()
+    _call(dev, "bsfp4_block_norm_backward", lib.bsfp4_block_norm_backward, (ctypes.byref(a),),
+          lib.bsfp4_block_norm_backward_workspace_size(T, H, a.groups))
+    return dx, dresidual, dw_post, dw_pre, dgate
 
 
 def e2m1_convert(values: torch.Tensor, scale_codes: torch.Tensor | None = None) -> torch.Tensor:

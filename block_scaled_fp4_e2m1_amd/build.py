@@ -29,6 +29,10 @@ SOURCES = [
     "gemm_w4a16.hip",
     "moe.hip",
     "moe_nvfp4.hip",
+    "int8_quant.hip",
+    "gemm_int8.hip",
+    "gated_ffn.hip",
+    "block_norm.hip",
     "layout.hip",
     "e2m1_convert.hip",
     "scratch.hip",

@@ -295,6 +295,311 @@ bsfp4_status w4a16_gemm(const uint16_t* A, const uint8_t* B, const uint8_t* SFB,
   return ok();
 }
 
+// ------------------------------------------------------------------ 8-bit integers
+
+namespace {
+
+// Largest row of a tiled operand in bytes (32-bit lane offsets over 256 rows).
+constexpr int64_t kTileRowBytes = (int64_t)1 << 23;
+
+bsfp4_status check_rows_cols(const char* rows_name, int64_t M, const char* cols_name, int64_t N, int64_t n_step,
+                             const char* k_name, int64_t K, int64_t k_step) {
+  if (M < 0 || N <= 0 || K <= 0)
+    return fail(BSFP4_ERR_SHAPE, "need %s >= 0, %s > 0, %s > 0 (%lld, %lld, %lld)", rows_name, cols_name, k_name,
+                (long long)M, (long long)N, (long long)K);
+  if (N % n_step)
+    return fail(BSFP4_ERR_SHAPE, "%s=%lld is not a multiple of %lld", cols_name, (long long)N, (long long)n_step);
+  if (K % k_step)
+    return fail(BSFP4_ERR_SHAPE, "%s=%lld is not a multiple of %lld", k_name, (long long)K, (long long)k_step);
+  if (M > INT32_MAX || N > INT32_MAX / 2) return fail(BSFP4_ERR_SHAPE, "dimensions must fit in 31 bits");
+  if (M > ((int64_t)1 << 40) / N) return fail(BSFP4_ERR_SHAPE, "%s * %s exceeds 2^40", rows_name, cols_name);
+  return BSFP4_OK;
+}
+
+bsfp4_status check_int8_k(int64_t K) {
+  if (K > 131056)
+    return fail(BSFP4_ERR_SHAPE, "K=%lld exceeds 131056 (the 32-bit integer sum)", (long long)K);
+  return BSFP4_OK;
+}
+
+bsfp4_status check_workspace(const void* ws, size_t ws_bytes, size_t need) {
+  if (need == 0) return BSFP4_OK;
+  if (ws == nullptr || ws_bytes < need)
+    return fail(BSFP4_ERR_WORKSPACE, "workspace %zu bytes < required %zu", ws == nullptr ? 0 : ws_bytes, need);
+  if (!aligned(ws, 16)) return fail(BSFP4_ERR_ALIGNMENT, "ws is not 16-byte aligned");
+  return BSFP4_OK;
+}
+
+bsfp4_status check_act(int act) {
+  if (act != BSFP4_ACT_SILU && act != BSFP4_ACT_GELU && act != BSFP4_ACT_GELU_TANH)
+    return fail(BSFP4_ERR_INVALID_ARG, "unknown activation %d", act);
+  return BSFP4_OK;
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace
+
+bsfp4_status bsfp4_int8_quantize(const uint16_t* x, int64_t M, int64_t K, int8_t* q, float* s, void* stream) {
+  if (M < 0 || K <= 0)
+    return fail(BSFP4_ERR_SHAPE, "need M >= 0 and K > 0 (M=%lld K=%lld)", (long long)M, (long long)K);
+  if (K % 8) return fail(BSFP4_ERR_SHAPE, "K=%lld is not a multiple of 8", (long long)K);
+  if (M > INT32_MAX || K > INT32_MAX) return fail(BSFP4_ERR_SHAPE, "dimensions must fit in 31 bits");
+  if (M == 0) return ok();
+  REQUIRE_PTR(x);
+  REQUIRE_PTR(q);
+  REQUIRE_SCALAR_PTR(s);
+  if (bsfp4_status e = check_device()) return e;
+  return launched(bsfp4::launch_int8_quant(x, M, K, q, s, as_stream(stream)), "bsfp4_int8_quantize launch");
+}
+
+size_t bsfp4_int8_gemm_workspace_size(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || K <= 0) return 0;
+  return bsfp4::int8_gemm_workspace(M, N, K);
+}
+
+bsfp4_status bsfp4_int8_gemm(const int8_t* A, const float* sa, const int8_t* B, const float* sb, const uint16_t* bias,
+                             uint16_t* D, int64_t M, int64_t N, int64_t K, void* ws, size_t ws_bytes, void* stream) {
+  if (bsfp4_status e = check_rows_cols("M", M, "N", N, 8, "K", K, 16)) return e;
+  if (bsfp4_status e = check_int8_k(K)) return e;
+  if (M > 0) {
+    REQUIRE_PTR(A);
+    REQUIRE_SCALAR_PTR(sa);
+    REQUIRE_PTR(D);
+  }
+  REQUIRE_PTR(B);
+  REQUIRE_PTR(sb);
+  if (bias != nullptr && !aligned(bias, 16)) return fail(BSFP4_ERR_ALIGNMENT, "bias is not 16-byte aligned");
+  if (bsfp4_status e = check_workspace(ws, ws_bytes, bsfp4_int8_gemm_workspace_size(M, N, K))) return e;
+  if (M == 0) return ok();
+  if (bsfp4_status e = check_device()) return e;
+  return launched(bsfp4::launch_int8_gemm(A, sa, B, sb, bias, D, M, N, K, ws, as_stream(stream)),
+                  "bsfp4_int8_gemm launch");
+}
+
+size_t bsfp4_int8_quantize_gemm_workspace_size(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || K <= 0) return 0;
+  return round256((size_t)M * K) + round256((size_t)M * sizeof(float)) + bsfp4::int8_gemm_workspace(M, N, K);
+}
+
+bsfp4_status bsfp4_int8_quantize_gemm(const uint16_t* x, const int8_t* B, const float* sb, const uint16_t* bias,
+                                      uint16_t* D, int64_t M, int64_t N, int64_t K, void* ws, size_t ws_bytes,
+                                      void* stream) {
+  if (bsfp4_status e = check_rows_cols("M", M, "N", N, 8, "K", K, 16)) return e;
+  if (bsfp4_status e = check_int8_k(K)) return e;
+  if (M > 0) {
+    REQUIRE_PTR(x);
+    REQUIRE_PTR(D);
+  }
+  REQUIRE_PTR(B);
+  REQUIRE_PTR(sb);
+  if (bias != nullptr && !aligned(bias, 16)) return fail(BSFP4_ERR_ALIGNMENT, "bias is not 16-byte aligned");
+  if (bsfp4_status e = check_workspace(ws, ws_bytes, bsfp4_int8_quantize_gemm_workspace_size(M, N, K))) return e;
+  if (M == 0) return ok();
+  if (bsfp4_status e = check_device()) return e;
+  int8_t* q = static_cast<int8_t*>(ws);
+  float* s = reinterpret_cast<float*>(q + round256((size_t)M * K));
+  void* rest = reinterpret_cast<uint8_t*>(s) + round256((size_t)M * sizeof(float));
+  hipError_t e = bsfp4::launch_int8_quant(x, M, K, q, s, as_stream(stream));
+  if (e == hipSuccess) e = bsfp4::launch_int8_gemm(q, s, B, sb, bias, D, M, N, K, rest, as_stream(stream));
+  return launched(e, "bsfp4_int8_quantize_gemm launch");
+}
+
+size_t bsfp4_int8_gated_ffn_workspace_size(int64_t M, int64_t I, int64_t K) {
+  if (M <= 0 || I <= 0 || K <= 0) return 0;
+  return bsfp4::int8_gated_workspace(M, I, K);
+}
+
+bsfp4_status bsfp4_int8_gated_ffn(const int8_t* A, const float* sa, const int8_t* W, const float* sw, int act,
+                                  uint16_t* h, int64_t M, int64_t I, int64_t K, void* ws, size_t ws_bytes,
+                                  void* stream) {
+  if (bsfp4_status e = check_act(act)) return e;
+  if (bsfp4_status e = check_rows_cols("M", M, "I", I, 8, "K", K, 16)) return e;
+  if (bsfp4_status e = check_int8_k(K)) return e;
+  if (M > 0) {
+    REQUIRE_PTR(A);
+    REQUIRE_SCALAR_PTR(sa);
+    REQUIRE_PTR(h);
+  }
+  REQUIRE_PTR(W);
+  REQUIRE_PTR(sw);
+  if (bsfp4_status e = check_workspace(ws, ws_bytes, bsfp4_int8_gated_ffn_workspace_size(M, I, K))) return e;
+  if (M == 0) return ok();
+  if (bsfp4_status e = check_device()) return e;
+  return launched(bsfp4::launch_int8_gated(A, sa, W, sw, act, h, M, I, K, ws, as_stream(stream)),
+                  "bsfp4_int8_gated_ffn launch");
+}
+
+// ------------------------------------------------------------------ gated feed-forward, bf16
+
+static bsfp4_status check_gated(int act, int64_t M, int64_t I, int64_t H) {
+  if (bsfp4_status e = check_act(act)) return e;
+  if (bsfp4_status e = check_rows_cols("M", M, "I", I, 8, "H", H, 8)) return e;
+  if (2 * H >= kTileRowBytes || 4 * I >= kTileRowBytes)
+    return fail(BSFP4_ERR_SHAPE, "need H < 2^22 and I < 2^21 (H=%lld I=%lld)", (long long)H, (long long)I);
+  if (M > ((int64_t)1 << 40) / H) return fail(BSFP4_ERR_SHAPE, "M * H exceeds 2^40");
+  return BSFP4_OK;
+}
+
+size_t bsfp4_gated_ffn_workspace_size(int64_t M, int64_t I, int64_t H) {
+  if (M <= 0 || I <= 0 || H <= 0) return 0;
+  return bsfp4::gated_ffn_workspace(M, I, H);
+}
+
+bsfp4_status bsfp4_gated_ffn(const uint16_t* x, const uint16_t* W, int act, uint16_t* h, uint16_t* gate_up, int64_t M,
+                             int64_t I, int64_t H, void* ws, size_t ws_bytes, void* stream) {
+  if (bsfp4_status e = check_gated(act, M, I, H)) return e;
+  if (M > 0) {
+    REQUIRE_PTR(x);
+    REQUIRE_PTR(h);
+  }
+  REQUIRE_PTR(W);
+  if (gate_up != nullptr && !aligned(gate_up, 16)) return fail(BSFP4_ERR_ALIGNMENT, "gate_up is not 16-byte aligned");
+  if (bsfp4_status e = check_workspace(ws, ws_bytes, bsfp4_gated_ffn_workspace_size(M, I, H))) return e;
+  if (M == 0) return ok();
+  if (bsfp4_status e = check_device()) return e;
+  return launched(bsfp4::launch_gated_ffn(x, W, act, h, gate_up, M, I, H, ws, as_stream(stream)),
+                  "bsfp4_gated_ffn launch");
+}
+
+size_t bsfp4_gated_ffn_backward_workspace_size(int64_t M, int64_t I, int64_t H) {
+  if (M < 0 || I <= 0 || H <= 0) return 0;
+  return bsfp4::gated_ffn_bwd_workspace(M, I, H);
+}
+
+bsfp4_status bsfp4_gated_ffn_backward(const uint16_t* dh, const uint16_t* x, const uint16_t* W,
+                                      const uint16_t* gate_up, int act, uint16_t* dx, uint16_t* dW, int64_t M,
+                                      int64_t I, int64_t H, void* ws, size_t ws_bytes, void* stream) {
+  if (bsfp4_status e = check_gated(act, M, I, H)) return e;
+  if (M > 0) {
+    REQUIRE_PTR(dh);
+    REQUIRE_PTR(gate_up);
+    if (dx != nullptr) REQUIRE_PTR(W);
+    if (dW != nullptr) REQUIRE_PTR(x);
+  }
+  if (dx == nullptr && dW == nullptr) return fail(BSFP4_ERR_INVALID_ARG, "dx and dW are both NULL");
+  if (dx != nullptr && !aligned(dx, 16)) return fail(BSFP4_ERR_ALIGNMENT, "dx is not 16-byte aligned");
+  if (dW != nullptr && !aligned(dW, 16)) return fail(BSFP4_ERR_ALIGNMENT, "dW is not 16-byte aligned");
+  if (bsfp4_status e = check_workspace(ws, ws_bytes, bsfp4_gated_ffn_backward_workspace_size(M, I, H))) return e;
+  if (M == 0 && dW == nullptr) return ok();
+  if (bsfp4_status e = check_device()) return e;
+  return launched(bsfp4::launch_gated_ffn_bwd(dh, x, W, gate_up, act, M == 0 ? nullptr : dx, dW, M, I, H, ws,
+                                              as_stream(stream)),
+                  "bsfp4_gated_ffn_backward launch");
+}
+
+// ------------------------------------------------------------------ block norms
+
+namespace {
+
+bsfp4_status check_block_norm(const bsfp4_block_norm_args* a) {
+  if (a == nullptr) return fail(BSFP4_ERR_INVALID_ARG, "args is NULL");
+  if (a->T < 0 || a->H <= 0 || a->groups <= 0)
+    return fail(BSFP4_ERR_SHAPE, "need T >= 0, H > 0, groups > 0 (T=%lld H=%lld groups=%lld)", (long long)a->T,
+                (long long)a->H, (long long)a->groups);
+  if (a->H % 8) return fail(BSFP4_ERR_SHAPE, "H=%lld is not a multiple of 8", (long long)a->H);
+  if (a->H > bsfp4::kBlockNormMaxH)
+    return fail(BSFP4_ERR_SHAPE, "H=%lld exceeds %lld", (long long)a->H, (long long)bsfp4::kBlockNormMaxH);
+  if (a->T > INT32_MAX || a->groups > INT32_MAX) return fail(BSFP4_ERR_SHAPE, "dimensions must fit in 31 bits");
+  if (a->T % a->groups)
+    return fail(BSFP4_ERR_SHAPE, "T=%lld is not a multiple of groups=%lld", (long long)a->T, (long long)a->groups);
+  if (!(a->eps > 0.0 && a->eps < 1e30)) return fail(BSFP4_ERR_INVALID_ARG, "eps must be positive and finite");
+  // (no rows: the row tensors may be NULL whatever the vectors are)
+  if (a->T > 0 && a->x == nullptr && (a->w_post != nullptr || a->gate != nullptr))
+    return fail(BSFP4_ERR_INVALID_ARG, "without x there is no w_post and no gate");
+  if (a->T > 0 && a->x == nullptr && a->w_pre == nullptr) return fail(BSFP4_ERR_INVALID_ARG, "neither x nor w_pre is given");
+  if (a->gate == nullptr && a->groups != 1) return fail(BSFP4_ERR_SHAPE, "groups must be 1 without a gate");
+  const struct {
+    const void* p;
+    const char* name;
+  } ptrs[] = {{a->x, "x"},           {a->residual, "residual"}, {a->w_post, "w_post"},     {a->w_pre, "w_pre"},
+              {a->gate, "gate"},     {a->res_out, "res_out"},   {a->z, "z"},               {a->q, "q"},
+              {a->dres_out, "dres_out"}, {a->dz, "dz"},         {a->dx, "dx"},             {a->dres, "dres"},
+              {a->dw_post, "dw_post"},   {a->dw_pre, "dw_pre"}, {a->dgate, "dgate"}};
+  for (const auto& q : ptrs)
+    if (!aligned(q.p, 16)) return fail(BSFP4_ERR_ALIGNMENT, "%s is not 16-byte aligned", q.name);
+  if (!aligned(a->s, 4)) return fail(BSFP4_ERR_ALIGNMENT, "s is not 4-byte aligned");
+  return BSFP4_OK;
+}
+
+bsfp4::BlockNormArgs norm_args(const bsfp4_block_norm_args* a) {
+  bsfp4::BlockNormArgs p{};
+  p.x = a->x;
+  p.residual = a->residual;
+  p.w_post = a->w_post;
+  p.w_pre = a->w_pre;
+  p.gate = a->gate;
+  p.scale = (float)a->scale;
+  p.eps = a->eps;
+  p.T = a->T;
+  p.groups = a->groups;
+  p.group_rows = a->T / a->groups;
+  p.H = (int)a->H;
+  return p;
+}
+
+#define REQUIRE_FIELD(f) \
+  if (a->f == nullptr) return fail(BSFP4_ERR_INVALID_ARG, #f " is NULL")
+
+}  // namespace
+
+bsfp4_status bsfp4_block_norm(const bsfp4_block_norm_args* a, void* stream) {
+  if (bsfp4_status e = check_block_norm(a)) return e;
+  if ((a->q == nullptr) != (a->s == nullptr)) return fail(BSFP4_ERR_INVALID_ARG, "q and s go together");
+  if (a->z != nullptr && a->q != nullptr) return fail(BSFP4_ERR_INVALID_ARG, "z and q are both given");
+  if (a->w_pre == nullptr && (a->z != nullptr || a->q != nullptr))
+    return fail(BSFP4_ERR_INVALID_ARG, "z or q without w_pre");
+  if (a->T == 0) return ok();
+  REQUIRE_FIELD(residual);
+  if (a->x != nullptr) REQUIRE_FIELD(res_out);
+  if (a->w_pre != nullptr && a->z == nullptr && a->q == nullptr)
+    return fail(BSFP4_ERR_INVALID_ARG, "w_pre without z or q");
+  if (bsfp4_status e = check_device()) return e;
+  bsfp4::BlockNormArgs p = norm_args(a);
+  p.res_out = a->res_out;
+  p.z = a->z;
+  p.q = a->q;
+  p.s = a->s;
+  return launched(bsfp4::launch_block_norm(p, as_stream(stream)), "bsfp4_block_norm launch");
+}
+
+size_t bsfp4_block_norm_backward_workspace_size(int64_t T, int64_t H, int64_t groups) {
+  if (T < 0 || H <= 0 || groups <= 0 || T % groups) return 0;
+  return bsfp4::block_norm_bwd_workspace(T, H, groups);
+}
+
+bsfp4_status bsfp4_block_norm_backward(const bsfp4_block_norm_args* a, void* ws, size_t ws_bytes, void* stream) {
+  if (bsfp4_status e = check_block_norm(a)) return e;
+  if (a->w_pre == nullptr && a->dz != nullptr) return fail(BSFP4_ERR_INVALID_ARG, "dz without w_pre");
+  if (a->T > 0) {
+    if (a->w_pre != nullptr) {
+      REQUIRE_FIELD(res_out);
+      REQUIRE_FIELD(dz);
+    } else {
+      REQUIRE_FIELD(dres_out);
+    }
+    if (a->x != nullptr) REQUIRE_FIELD(dx);
+    REQUIRE_FIELD(dres);
+  }
+  if (a->w_post != nullptr) REQUIRE_FIELD(dw_post);
+  if (a->w_pre != nullptr) REQUIRE_FIELD(dw_pre);
+  if (a->gate != nullptr) REQUIRE_FIELD(dgate);
+  if (bsfp4_status e = check_workspace(ws, ws_bytes, bsfp4_block_norm_backward_workspace_size(a->T, a->H, a->groups)))
+    return e;
+  if (bsfp4_status e = check_device()) return e;
+  bsfp4::BlockNormArgs p = norm_args(a);
+  p.res = a->res_out;
+  p.dres_out = a->dres_out;
+  p.dz = a->dz;
+  p.dx = a->dx;
+  p.dres = a->dres;
+  p.dw_post = a->dw_post;
+  p.dw_pre = a->dw_pre;
+  p.dgate = a->dgate;
+  return launched(bsfp4::launch_block_norm_bwd(p, static_cast<float*>(ws), as_stream(stream)),
+                  "bsfp4_block_norm_backward launch");
+}
+
 // ------------------------------------------------------------------ E2M1 conversion
 
 bsfp4_status bsfp4_e2m1_convert(int mode, const void* in, const uint8_t* scale_codes, int64_t pairs,

@@ -1,0 +1,427 @@
+// RMS norms around a block, fused with the gate, the branch scale and the
+// residual add, forward and backward.
+//
+// Forward, per row (token) of H values:
+//   n  = x * rstd(x) * w_post                 (x itself without w_post)
+//   r' = bf16(r + (gate * scale) * n)
+//   z  = bf16(r' * rstd(r') * w_pre)           (bf16 rows, or 8-bit rows with a scale)
+//   rstd(v) = fl32(1 / sqrt(mean(v^2) + eps))
+// gate is [G, H]: T / G consecutive rows share a gate row.  The next norm reads
+// the residual row as it is stored (rounded to bf16).
+//
+// Every elementwise step is one binary32 operation in the order written.  The
+// mean squares are summed in 64 bits: squares of bf16 values are exact there and
+// the order of the sum moves the 32-bit rstd practically never, so a row's bytes
+// (its 8-bit codes in particular) do not depend on how many threads hold it.
+//
+// Backward, with rs = rstd(r'), xs = rstd(x), zh = r' rs, xh = x xs, mean over the row:
+//   gz = dz w_pre,  d = dr' + rs (gz - zh mean(gz zh)),  dr = bf16(d)
+//   dn = d (gate scale),  gx = dn w_post,  dx = xs (gx - xh mean(gx xh))
+//   dw_pre = sum_rows dz zh,  dw_post = sum_rows dn xh,  dgate = sum_group d scale n
+// Both means need only sums of stored values (mean(gz zh) = rs sum(gz r') / H),
+// so a row takes two reductions: {sum x^2, sum r'^2, sum gz r'} and {sum gx x}.
+//
+// Bound by memory: forward 4 H bytes read and 4 H (3 H) written per row, backward
+// 8 H read and 4 H written; the row stays in registers between the reductions.
+#include <algorithm>
+
+#include "int8_rows.h"
+#include "launchers.h"
+
+#pragma clang fp contract(off)
+
+namespace bsfp4 {
+namespace {
+
+// fl32(1 / sqrt(sum / H + eps)): the hardware's 64-bit estimate and two Newton
+// steps, y (1.5 - 0.5 v y^2), leave an error far below half a 32-bit unit.
+__device__ __forceinline__ float rstd_of(double sum, int H, double eps) {
+  const double v = sum / (double)H + eps;
+  double y = __builtin_amdgcn_rsq(v);
+  if (v < __builtin_inf()) {
+#pragma unroll
+    for (int i = 0; i < 2; i++) y = y * (1.5 - 0.5 * v * y * y);
+  }
+  return (float)y;
+}
+
+__device__ __forceinline__ double sumsq8(const uint4& c, double s) {
+  float v[8];
+  unpack8(c, v);
+#pragma unroll
+  for (int j = 0; j < 8; j++) s = __builtin_fma((double)v[j], (double)v[j], s);
+  return s;
+}
+
+__device__ __forceinline__ uint4 chunk_or_zero(const uint16_t* row, int i, bool live) {
+  return live ? reinterpret_cast<const uint4*>(row)[i] : make_uint4(0, 0, 0, 0);
+}
+
+template <int NT, int CH, bool kInt8>
+__global__ void __launch_bounds__(NT < 256 ? 256 : NT)
+    block_norm_fwd(const BlockNormArgs p) {
+  constexpr int kRows = NT < 256 ? 256 / NT : 1;
+  static_assert(kRows == 1 || NT == 64, "several rows per workgroup: a wave each");
+  __shared__ double red[2][NT / 64];
+  __shared__ uint32_t redm[NT / 64];
+  const int t = kRows > 1 ? (int)(threadIdx.x % NT) : (int)threadIdx.x;
+  const int64_t m = (int64_t)blockIdx.x * kRows + (kRows > 1 ? threadIdx.x / NT : 0);
+  if (m >= p.T) return;
+  const int H = p.H, chunks = H / 8;
+  const int64_t off = m * (int64_t)H;
+  uint4 x[CH], r[CH], wp[CH], gt[CH], wn[CH];
+#pragma unroll
+  for (int j = 0; j < CH; j++) {
+    const int i = t + j * NT;
+    const bool live = i < chunks;
+    if (p.x) x[j] = chunk_or_zero(p.x + off, i, live);
+    r[j] = chunk_or_zero(p.residual + off, i, live);
+    if (p.w_post) wp[j] = chunk_or_zero(p.w_post, i, live);
+    if (p.gate) gt[j] = chunk_or_zero(p.gate + (m / p.group_rows) * H, i, live);
+    if (p.w_pre) wn[j] = chunk_or_zero(p.w_pre, i, live);
+  }
+  if (p.x) {
+    float xs = 1.0f;
+    if (p.w_post) {
+      double s[1] = {0.0};
+#pragma unroll
+      for (int j = 0; j < CH; j++) s[0] = sumsq8(x[j], s[0]);
+      row_sum<NT>(s, red[0]);
+      xs = rstd_of(s[0], H, p.eps);
+    }
+#pragma unroll
+    for (int j = 0; j < CH; j++) {
+      float xv[8], rv[8], wv[8], gv[8];
+      unpack8(x[j], xv);
+      unpack8(r[j], rv);
+      if (p.w_post) unpack8(wp[j], wv);
+      if (p.gate) unpack8(gt[j], gv);
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        const float n = p.w_post ? xv[k] * xs * wv[k] : xv[k];
+        const float g = p.gate ? gv[k] * p.scale : p.scale;
+        rv[k] = rv[k] + g * n;
+      }
+      r[j] = pack8(rv);
+      const int i = t + j * NT;
+      if (i < chunks) reinterpret_cast<uint4*>(p.res_out + off)[i] = r[j];
+    }
+  }
+  if (!p.w_pre) return;
+  double s[1] = {0.0};
+#pragma unroll
+  for (int j = 0; j < CH; j++) s[0] = sumsq8(r[j], s[0]);
+  row_sum<NT>(s, red[1]);
+  const float rs = rstd_of(s[0], H, p.eps);
+  uint32_t mx = 0;
+#pragma unroll
+  for (int j = 0; j < CH; j++) {
+    float rv[8], wv[8];
+    unpack8(r[j], rv);
+    unpack8(wn[j], wv);
+#pragma unroll
+    for (int k = 0; k < 8; k++) rv[k] = rv[k] * rs * wv[k];
+    r[j] = pack8(rv);
+    const int i = t + j * NT;
+    if constexpr (kInt8) {
+      // lanes past the row hold zeros times a finite or infinite rstd: keep them out
+      if (i < chunks) mx = amax_bits8(r[j], mx);
+    } else {
+      if (i < chunks) reinterpret_cast<uint4*>(p.z + off)[i] = r[j];
+    }
+  }
+  if constexpr (kInt8) {
+    const Int8Row q(row_max<NT>(mx, redm));
+#pragma unroll
+    for (int j = 0; j < CH; j++) {
+      const int i = t + j * NT;
+      if (i < chunks) reinterpret_cast<uint2*>(p.q + off)[i] = q.codes8(r[j]);
+    }
+    if (t == 0) p.s[m] = q.s;
+  }
+}
+
+// One workgroup of NT threads walks the rows of a strip with its columns' three
+// vector gradients in registers.  Strips are either 1 / S of a gate group (the
+// group's dgate is then summed over S partials), or whole groups (its dgate is
+// final).  CH 16-byte chunks per thread: 1 up to H = 8 NT.
+template <int NT, int CH>
+__global__ void __launch_bounds__(NT)
+    block_norm_bwd(const BlockNormArgs p) {
+  __shared__ double red_a[3 * (NT / 64)];
+  __shared__ double red_b[NT / 64];
+  const int t = threadIdx.x;
+  const int H = p.H, chunks = H / 8;
+  const bool has_x = p.x != nullptr, has_post = p.w_post != nullptr, has_pre = p.w_pre != nullptr,
+             has_gate = p.gate != nullptr, has_dres = p.dres_out != nullptr;
+  const int64_t strip = blockIdx.x;
+  int64_t g0, g1, part = 0, parts = 1;
+  if (p.strips_per_group > 1) {
+    parts = p.strips_per_group;
+    g0 = strip / parts;
+    g1 = g0 + 1;
+    part = strip % parts;
+  } else {
+    g0 = strip * p.groups_per_strip;
+    g1 = min(g0 + p.groups_per_strip, p.groups);
+  }
+  float apost[CH][8] = {}, apre[CH][8] = {};
+  uint4 wp[CH], wn[CH];
+#pragma unroll
+  for (int j = 0; j < CH; j++) {
+    const int i = t + j * NT;
+    if (has_post) wp[j] = chunk_or_zero(p.w_post, i, i < chunks);
+    if (has_pre) wn[j] = chunk_or_zero(p.w_pre, i, i < chunks);
+  }
+  for (int64_t g = g0; g < g1; g++) {
+    const int64_t ra = g * p.group_rows + p.group_rows * part / parts;
+    const int64_t rb = g * p.group_rows + p.group_rows * (part + 1) / parts;
+    float agate[CH][8] = {};
+    uint4 gt[CH];
+#pragma unroll
+    for (int j = 0; j < CH; j++) {
+      const int i = t + j * NT;
+      if (has_gate) gt[j] = chunk_or_zero(p.gate + g * H, i, i < chunks);
+    }
+    uint4 nx[CH], nr[CH], nz[CH], nd[CH];  // the next row's chunks
+    auto load = [&](int64_t m) {
+      const int64_t off = m * H;
+#pragma unroll
+      for (int j = 0; j < CH; j++) {
+        const int i = t + j * NT;
+        const bool live = i < chunks && m < rb;
+        if (has_x) nx[j] = chunk_or_zero(p.x + off, i, live);
+        if (has_pre) nr[j] = chunk_or_zero(p.res + off, i, live);
+        if (has_pre) nz[j] = chunk_or_zero(p.dz + off, i, live);
+        if (has_dres) nd[j] = chunk_or_zero(p.dres_out + off, i, live);
+      }
+    };
+    load(ra);
+    for (int64_t m = ra; m < rb; m++) {
+      uint4 x[CH], r[CH], z[CH], d4[CH];
+#pragma unroll
+      for (int j = 0; j < CH; j++) {
+        x[j] = nx[j];
+        r[j] = nr[j];
+        z[j] = nz[j];
+        d4[j] = nd[j];
+      }
+      load(m + 1);
+      double s[3] = {0.0, 0.0, 0.0};
+#pragma unroll
+      for (int j = 0; j < CH; j++) {
+        if (has_x && has_post) s[0] = sumsq8(x[j], s[0]);
+        if (has_pre) {
+          s[1] = sumsq8(r[j], s[1]);
+          float rv[8], zv[8], wv[8], dot = 0.0f;
+          unpack8(r[j], rv);
+          unpack8(z[j], zv);
+          unpack8(wn[j], wv);
+#pragma unroll
+          for (int k = 0; k < 8; k++) dot = __builtin_fmaf(zv[k] * wv[k], rv[k], dot);
+          s[2] += (double)dot;
+        }
+      }
+      row_sum<NT>(s, red_a);
+      const float xs = has_x && has_post ? rstd_of(s[0], H, p.eps) : 1.0f;
+      const float rs = has_pre ? rstd_of(s[1], H, p.eps) : 1.0f;
+      const float mz = (float)(s[2] / (double)H * (double)rs);  // mean(gz zh)
+      float d[CH][8];
+      double sb[1] = {0.0};
+#pragma unroll
+      for (int j = 0; j < CH; j++) {
+        float rv[8], zv[8], wv[8];
+        if (has_dres) {
+          unpack8(d4[j], d[j]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; k++) d[j][k] = 0.0f;
+        }
+        if (has_pre) {
+          unpack8(r[j], rv);
+          unpack8(z[j], zv);
+          unpack8(wn[j], wv);
+#pragma unroll
+          for (int k = 0; k < 8; k++) {
+            const float zh = rv[k] * rs;
+            d[j][k] += rs * (zv[k] * wv[k] - zh * mz);
+            apre[j][k] += zv[k] * zh;
+          }
+        }
+        const int i = t + j * NT;
+        if (i < chunks && p.dres) reinterpret_cast<uint4*>(p.dres + m * H)[i] = pack8(d[j]);
+        if (has_x) {
+          float xv[8], pv[8], gv[8], dot = 0.0f;
+          unpack8(x[j], xv);
+          if (has_post) unpack8(wp[j], pv);
+          if (has_gate) unpack8(gt[j], gv);
+#pragma unroll
+          for (int k = 0; k < 8; k++) {
+            const float xh = xv[k] * xs;
+            const float n = has_post ? xh * pv[k] : xh;
+            if (has_gate) agate[j][k] += d[j][k] * p.scale * n;
+            const float dn = d[j][k] * (has_gate ? gv[k] * p.scale : p.scale);
+            if (has_post) apost[j][k] += dn * xh;
+            d[j][k] = has_post ? dn * pv[k] : dn;  // gx from here on
+            dot = __builtin_fmaf(d[j][k], xv[k], dot);
+          }
+          sb[0] += (double)dot;
+        }
+      }
+      if (has_x) {
+        float mx = 0.0f;  // mean(gx xh) xs
+        if (has_post) {
+          row_sum<NT>(sb, red_b);
+          mx = (float)(sb[0] / (double)H * (double)xs);
+        }
+#pragma unroll
+        for (int j = 0; j < CH; j++) {
+          if (has_post) {
+            float xv[8];
+            unpack8(x[j], xv);
+#pragma unroll
+            for (int k = 0; k < 8; k++) d[j][k] = xs * (d[j][k] - xv[k] * xs * mx);
+          }
+          const int i = t + j * NT;
+          if (i < chunks) reinterpret_cast<uint4*>(p.dx + m * H)[i] = pack8(d[j]);
+        }
+      }
+    }
+    if (has_gate) {
+      float* dst = parts > 1 ? p.part_gate + strip * H : p.dgate + g * H;
+#pragma unroll
+      for (int j = 0; j < CH; j++) {
+        const int i = t + j * NT;
+        if (i < chunks) {
+          reinterpret_cast<float4*>(dst)[2 * i] = make_float4(agate[j][0], agate[j][1], agate[j][2], agate[j][3]);
+          reinterpret_cast<float4*>(dst)[2 * i + 1] = make_float4(agate[j][4], agate[j][5], agate[j][6], agate[j][7]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < CH; j++) {
+    const int i = t + j * NT;
+    if (i >= chunks) continue;
+    if (has_post) {
+      float4* dst = reinterpret_cast<float4*>(p.part_post + strip * H);
+      dst[2 * i] = make_float4(apost[j][0], apost[j][1], apost[j][2], apost[j][3]);
+      dst[2 * i + 1] = make_float4(apost[j][4], apost[j][5], apost[j][6], apost[j][7]);
+    }
+    if (has_pre) {
+      float4* dst = reinterpret_cast<float4*>(p.part_pre + strip * H);
+      dst[2 * i] = make_float4(apre[j][0], apre[j][1], apre[j][2], apre[j][3]);
+      dst[2 * i + 1] = make_float4(apre[j][4], apre[j][5], apre[j][6], apre[j][7]);
+    }
+  }
+}
+
+// out[h] = sum over strips of part[strip][h], in a fixed order: workgroups of 64
+// columns x 16 strip lanes.  blockIdx.y: 0 dw_post, 1 dw_pre, 2 + g dgate of group g.
+__global__ void __launch_bounds__(1024)
+    block_norm_sum(const BlockNormArgs p, int64_t strips) {
+  __shared__ float red[16][64];
+  const int which = blockIdx.y;
+  const float* src;
+  float* dst;
+  int64_t n = strips;
+  if (which == 0) {
+    src = p.part_post;
+    dst = p.dw_post;
+  } else if (which == 1) {
+    src = p.part_pre;
+    dst = p.dw_pre;
+  } else {
+    n = p.strips_per_group;
+    src = p.part_gate ? p.part_gate + (int64_t)(which - 2) * n * p.H : nullptr;
+    dst = p.dgate ? p.dgate + (int64_t)(which - 2) * p.H : nullptr;
+  }
+  if (src == nullptr) return;
+  const int c = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int h = blockIdx.x * 64 + c;
+  float acc = 0.0f;
+  if (h < p.H) {
+#pragma unroll 4
+    for (int64_t s = w; s < n; s += 16) acc += src[s * p.H + h];
+  }
+  red[w][c] = acc;
+  __syncthreads();
+  if (w == 0 && h < p.H) {
+    float v = red[0][c];
+#pragma unroll
+    for (int i = 1; i < 16; i++) v += red[i][c];
+    dst[h] = v;
+  }
+}
+
+struct Strips {
+  int64_t per_group, groups_per_strip, count;
+};
+
+// Strips of about 16 rows or more, at most ~2 workgroups of 512 threads per CU.
+Strips plan_strips(int64_t T, int64_t groups) {
+  const int64_t want = std::min<int64_t>(512, std::max<int64_t>(1, (T + 15) / 16));
+  const int64_t rows = T / groups;
+  Strips s;
+  if (groups >= want) {
+    s.per_group = 1;
+    s.groups_per_strip = (groups + want - 1) / want;
+    s.count = (groups + s.groups_per_strip - 1) / s.groups_per_strip;
+  } else {
+    s.per_group = std::min<int64_t>(rows, (want + groups - 1) / groups);
+    s.groups_per_strip = 1;
+    s.count = groups * s.per_group;
+  }
+  return s;
+}
+
+}  // namespace
+
+size_t block_norm_bwd_workspace(int64_t T, int64_t H, int64_t groups) {
+  return (size_t)plan_strips(T, groups).count * H * 3 * sizeof(float);
+}
+
+hipError_t launch_block_norm(const BlockNormArgs& p, hipStream_t stream) {
+  const int chunks = p.H / 8;
+#define BSFP4_FWD(NT, CH)                                                                              \
+  do {                                                                                                 \
+    const unsigned grid = (unsigned)(NT < 256 ? (p.T + 256 / NT - 1) / (256 / NT) : p.T);              \
+    if (p.q)                                                                                           \
+      block_norm_fwd<NT, CH, true><<<grid, NT < 256 ? 256 : NT, 0, stream>>>(p);                       \
+    else                                                                                               \
+      block_norm_fwd<NT, CH, false><<<grid, NT < 256 ? 256 : NT, 0, stream>>>(p);                      \
+  } while (0)
+  if (chunks <= 64) BSFP4_FWD(64, 1);
+  else if (chunks <= 256) BSFP4_FWD(256, 1);
+  else if (chunks <= 512) BSFP4_FWD(512, 1);
+  else if (chunks <= 1024) BSFP4_FWD(1024, 1);
+  else BSFP4_FWD(1024, 2);
+#undef BSFP4_FWD
+  return hipGetLastError();
+}
+
+hipError_t launch_block_norm_bwd(BlockNormArgs p, float* ws, hipStream_t stream) {
+  const Strips s = plan_strips(p.T, p.groups);
+  p.strips_per_group = s.per_group;
+  p.groups_per_strip = s.groups_per_strip;
+  const size_t n = (size_t)s.count * p.H;
+  p.part_post = p.w_post ? ws : nullptr;
+  p.part_pre = p.w_pre ? ws + n : nullptr;
+  p.part_gate = p.gate && s.per_group > 1 ? ws + 2 * n : nullptr;
+  const int chunks = p.H / 8;
+  const unsigned grid = (unsigned)s.count;
+  if (chunks <= 64) block_norm_bwd<64, 1><<<grid, 64, 0, stream>>>(p);
+  else if (chunks <= 128) block_norm_bwd<128, 1><<<grid, 128, 0, stream>>>(p);
+  else if (chunks <= 256) block_norm_bwd<256, 1><<<grid, 256, 0, stream>>>(p);
+  else if (chunks <= 512) block_norm_bwd<512, 1><<<grid, 512, 0, stream>>>(p);
+  else if (chunks <= 1024) block_norm_bwd<1024, 1><<<grid, 1024, 0, stream>>>(p);
+  else block_norm_bwd<1024, 2><<<grid, 1024, 0, stream>>>(p);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (!p.part_post && !p.part_pre && !p.part_gate) return hipSuccess;
+  const dim3 sg((unsigned)((p.H + 63) / 64), (unsigned)(2 + (p.part_gate ? p.groups : 0)));
+  block_norm_sum<<<sg, 1024, 0, stream>>>(p, s.count);
+  return hipGetLastError();
+}
+
+}  // namespace bsfp4

@@ -1,0 +1,127 @@
+// The gated feed-forward product in bf16 and its backward pass.
+//
+//   [G | U] = x W^T,  h = bf16(act(G) * U)            W [2 I, H]: gate rows, then up rows
+//   dG = dh U act'(G),  dU = dh act(G)                (from G, U as saved in bf16)
+//   dx = [dG | dU] W,   dW = [dG | dU]^T x
+//
+// Forward: one kernel, both projections of a column in one wave's accumulators, so
+// the activation and the product happen on binary32 sums and [G | U] is written
+// only when the backward pass is to follow (gate_up).
+// Backward: one pass writes [dG | dU] in bf16 (the matrix cores' operand type; its
+// rounding, like that of gate_up, is of the size of the outputs' own), then the
+// two products read W, x and [dG | dU] as they lie (transposed operands of
+// tile_gemm), with binary32 sums.
+#include "tile_gemm.h"
+
+namespace bsfp4 {
+namespace {
+
+__global__ void __launch_bounds__(256)
+    gated_grad(const uint16_t* __restrict__ dh, const uint16_t* __restrict__ gate_up, int act, int64_t M, int I,
+               uint16_t* __restrict__ dgu) {
+  const int chunks = I / 8;
+  const int64_t all = M * chunks, stride = (int64_t)gridDim.x * blockDim.x;
+  for (int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; idx < all; idx += stride) {
+    const int64_t m = idx / chunks;
+    const int64_t n = (idx - m * chunks) * 8, row = m * 2 * I;
+    float d[8], g[8], u[8], dg[8], du[8];
+    unpack8(*reinterpret_cast<const uint4*>(dh + m * I + n), d);
+    unpack8(*reinterpret_cast<const uint4*>(gate_up + row + n), g);
+    unpack8(*reinterpret_cast<const uint4*>(gate_up + row + I + n), u);
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+      float a, da;
+      act_value_grad(act, g[k], a, da);
+      dg[k] = d[k] * u[k] * da;
+      du[k] = d[k] * a;
+    }
+    *reinterpret_cast<uint4*>(dgu + row + n) = pack8(dg);
+    *reinterpret_cast<uint4*>(dgu + row + I + n) = pack8(du);
+  }
+}
+
+struct BwdPlan {
+  TilePlan dx, dw;
+  size_t dgu, part;  // workspace bytes of [dG | dU] and of the larger product's partials
+};
+
+BwdPlan plan_bwd(int64_t M, int64_t H, int64_t I) {
+  const int cus = device_cu_count();
+  BwdPlan b;
+  b.dx = plan_tile(M, H, 4 * I, cus);
+  b.dw = plan_tile(2 * I, H, 2 * M, cus);
+  b.dgu = ((size_t)M * 2 * I * 2 + 255) / 256 * 256;
+  b.part = std::max(tile_workspace(b.dx, M, H), tile_workspace(b.dw, 2 * I, H));
+  return b;
+}
+
+}  // namespace
+
+size_t gated_ffn_workspace(int64_t M, int64_t I, int64_t H) {
+  return tile_workspace(plan_tile(M, 2 * I, 2 * H, device_cu_count()), M, 2 * I);
+}
+
+hipError_t launch_gated_ffn(const uint16_t* x, const uint16_t* W, int act, uint16_t* h, uint16_t* gate_up, int64_t M,
+                            int64_t I, int64_t H, void* ws, hipStream_t stream) {
+  TileArgs a{};
+  a.A = reinterpret_cast<const uint8_t*>(x);
+  a.B = reinterpret_cast<const uint8_t*>(W);
+  a.lda = a.ldb = 2 * H;
+  a.M = (int)M;
+  a.N = (int)I;
+  a.kend = 2 * H;
+  a.act = act;
+  a.D = h;
+  a.gate_up = gate_up;
+  a.part = ws;
+  return launch_tile<false, false, false, kTileGated>(a, plan_tile(M, 2 * I, 2 * H, device_cu_count()), stream);
+}
+
+size_t gated_ffn_bwd_workspace(int64_t M, int64_t I, int64_t H) {
+  const BwdPlan b = plan_bwd(M, H, I);
+  return b.dgu + b.part;
+}
+
+hipError_t launch_gated_ffn_bwd(const uint16_t* dh, const uint16_t* x, const uint16_t* W, const uint16_t* gate_up,
+                                int act, uint16_t* dx, uint16_t* dW, int64_t M, int64_t I, int64_t H, void* ws,
+                                hipStream_t stream) {
+  const BwdPlan b = plan_bwd(M, H, I);
+  uint16_t* dgu = static_cast<uint16_t*>(ws);
+  void* part = static_cast<uint8_t*>(ws) + b.dgu;
+  const int64_t items = M * (I / 8);
+  hipError_t e = hipSuccess;
+  if (M > 0) {
+    gated_grad<<<(unsigned)std::min<int64_t>((items + 255) / 256, 8192), 256, 0, stream>>>(dh, gate_up, act, M,
+                                                                                           (int)I, dgu);
+    e = hipGetLastError();
+  }
+  if (e == hipSuccess && dx != nullptr) {
+    TileArgs a{};
+    a.A = reinterpret_cast<const uint8_t*>(dgu);
+    a.lda = 4 * I;
+    a.B = reinterpret_cast<const uint8_t*>(W);
+    a.ldb = 2 * H;
+    a.M = (int)M;
+    a.N = (int)H;
+    a.kend = 2 * I;  // k rows of W
+    a.D = dx;
+    a.part = part;
+    e = launch_tile<false, false, true, kTileStore>(a, b.dx, stream);
+  }
+  if (e == hipSuccess && dW != nullptr) {
+    TileArgs a{};
+    a.A = reinterpret_cast<const uint8_t*>(dgu);
+    a.lda = 4 * I;
+    a.B = reinterpret_cast<const uint8_t*>(x);
+    a.ldb = 2 * H;
+    a.M = (int)(2 * I);
+    a.N = (int)H;
+    a.kend = M;  // k rows of dgu and x
+    a.D = dW;
+    a.part = part;
+    e = launch_tile<false, true, true, kTileStore>(a, b.dw, stream);
+  }
+  return e;
+}
+
+}  // namespace bsfp4

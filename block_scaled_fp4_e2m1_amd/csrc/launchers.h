@@ -114,6 +114,58 @@ hipError_t launch_nvfp4_grouped(const uint8_t* Aq, const uint8_t* Asf, const int
                                 int64_t N, int64_t K, int epilogue, uint16_t* out, uint8_t* out_q, uint8_t* out_sf,
                                 const float* out_gs, const int32_t* sorted_ids, float* y, hipStream_t stream);
 
+// Per-token 8-bit rows of a bf16 matrix (K % 16 == 0).
+hipError_t launch_int8_quant(const uint16_t* x, int64_t M, int64_t K, int8_t* q, float* s, hipStream_t stream);
+
+// 8-bit products (gemm_int8.hip; K % 16 == 0, N % 8 == 0); gated: W [2 I, K].
+size_t int8_gemm_workspace(int64_t M, int64_t N, int64_t K);
+size_t int8_gated_workspace(int64_t M, int64_t I, int64_t K);
+hipError_t launch_int8_gemm(const int8_t* A, const float* sa, const int8_t* B, const float* sb, const uint16_t* bias,
+                            uint16_t* D, int64_t M, int64_t N, int64_t K, void* ws, hipStream_t stream);
+hipError_t launch_int8_gated(const int8_t* A, const float* sa, const int8_t* W, const float* sw, int act, uint16_t* D,
+                             int64_t M, int64_t I, int64_t K, void* ws, hipStream_t stream);
+
+// Gated feed-forward product in bf16 (gated_ffn.hip; H % 8 == 0, I % 8 == 0).
+constexpr int kActSilu = 0, kActGelu = 1, kActGeluTanh = 2;
+size_t gated_ffn_workspace(int64_t M, int64_t I, int64_t H);
+hipError_t launch_gated_ffn(const uint16_t* x, const uint16_t* W, int act, uint16_t* h, uint16_t* gate_up, int64_t M,
+                            int64_t I, int64_t H, void* ws, hipStream_t stream);
+size_t gated_ffn_bwd_workspace(int64_t M, int64_t I, int64_t H);
+hipError_t launch_gated_ffn_bwd(const uint16_t* dh, const uint16_t* x, const uint16_t* W, const uint16_t* gate_up,
+                                int act, uint16_t* dx, uint16_t* dW, int64_t M, int64_t I, int64_t H, void* ws,
+                                hipStream_t stream);
+
+// Norms around a block (block_norm.hip); null pointers leave a part out.
+struct BlockNormArgs {
+  const uint16_t* x;         // block output [T, H], or null: r' = residual, nothing added
+  const uint16_t* residual;  // [T, H] (forward)
+  const uint16_t* w_post;    // [H] or null
+  const uint16_t* w_pre;     // [H] or null
+  const uint16_t* gate;      // [groups, H] or null
+  float scale;
+  double eps;
+  int64_t T, groups, group_rows;  // group_rows = T / groups
+  int H;
+  uint16_t* res_out;  // forward: r' [T, H]
+  uint16_t* z;        // forward: bf16 [T, H], or q and s
+  int8_t* q;
+  float* s;
+  // backward
+  const uint16_t* res;       // r' [T, H] (with w_pre)
+  const uint16_t* dres_out;  // gradient of r', or null (zeros)
+  const uint16_t* dz;        // gradient of z (with w_pre)
+  uint16_t* dx;
+  uint16_t* dres;
+  float *dw_post, *dw_pre, *dgate;
+  // set by the launcher
+  float *part_post, *part_pre, *part_gate;
+  int64_t strips_per_group, groups_per_strip;
+};
+constexpr int64_t kBlockNormMaxH = 16384;
+size_t block_norm_bwd_workspace(int64_t T, int64_t H, int64_t groups);
+hipError_t launch_block_norm(const BlockNormArgs& p, hipStream_t stream);
+hipError_t launch_block_norm_bwd(BlockNormArgs p, float* ws, hipStream_t stream);
+
 // MoE routing prep and the combine's helpers.
 hipError_t launch_moe_prep(const int32_t* topk_ids, int64_t T, int64_t topk, int64_t E, int32_t* offsets,
                            int32_t* sorted_ids, int32_t* sorted_tokens, hipStream_t stream);

@@ -1,0 +1,572 @@
+// Tiled matrix product for bf16 and 8-bit integer operands, shared by the 8-bit
+// GEMM, the gated feed-forward products and their backward pass.
+//
+//   acc[m, n] = sum_k A(m, k) B(n, k)
+//
+// bf16 and int8 are the same kernel: a 16-byte chunk is 8 bf16 or 16 int8
+// values, v_mfma_f32_32x32x16_bf16 and v_mfma_i32_32x32x32_i8 each take one such
+// chunk per lane and operand, and both run 32 cycles, so everything is laid out
+// in bytes and only the instruction differs.
+//
+// Each operand is stored either with its rows along K (a row of A is one m, K
+// contiguous) or, for bf16, transposed (a row is one k): the backward pass reads
+// the weight and the activations that way.  A transposed tile stays k-major in
+// LDS and ds_read_b64_tr_b16 hands every lane its four consecutive k values, so
+// no transposed copy is ever written.
+//
+// Structure: a BM x BN tile per workgroup of WGM x WGN waves, K in stages of 128
+// bytes per row, two LDS slots filled by direct-to-LDS buffer loads (1 KB each),
+// the next stage's loads in flight while a stage is multiplied.
+// LDS layout of a stage, A first:
+//   rows along K   [rows][8 chunks of 16 B], chunk c of row r at position
+//                  c ^ ((r ^ r / 8) & 7): the 32 rows of a fragment read hit
+//                  distinct bank groups
+//   transposed     [64 k][BM or BN values] in 32-byte units, their pairs
+//                  exchanged by row (tile_tswz): the four k rows of a
+//                  transposing read hit distinct banks
+// Both swizzles are applied to the global address of each lane's 16 bytes, as the
+// LDS side of a direct load is always consecutive.
+//
+// Rows past the operand's end and chunks past K are read as zeros through the
+// buffer range check (kBufOOB lanes), so any M, any N and any K of whole 16-byte
+// chunks run through the same loop.
+#pragma once
+
+#include <algorithm>
+#include <type_traits>
+
+#include "device_common.h"
+#include "int8_rows.h"
+#include "launchers.h"
+#include "lds_dma.h"
+
+namespace bsfp4 {
+namespace {
+
+constexpr int kTileStage = 128;  // bytes of K per row and stage (rows along K)
+constexpr int kTileStageK = 64;  // k rows per stage (transposed bf16)
+
+typedef int v16i __attribute__((ext_vector_type(16)));
+
+template <bool kInt8>
+struct Mma;
+template <>
+struct Mma<false> {
+  typedef v16f Acc;
+  __device__ static __forceinline__ Acc run(v4i a, v4i b, Acc c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+  }
+};
+template <>
+struct Mma<true> {
+  typedef v16i Acc;
+  __device__ static __forceinline__ Acc run(v4i a, v4i b, Acc c) {
+    return __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0);
+  }
+};
+
+// ---- activations -----------------------------------------------------------
+// sigmoid with the hardware exp2 and reciprocal (a few binary32 ulp; results
+// are rounded to bf16)
+__device__ __forceinline__ float sigmoid_f(float v) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504088896341f));
+}
+
+// tanh form: 0.5 (1 + tanh u) = sigmoid(2 u), 2 u = kGeluC (g + 0.044715 g^3)
+constexpr float kGeluC = 1.59576912160573071f;  // sqrt(8 / pi)
+constexpr float kGeluA = 0.044715f;
+
+__device__ __forceinline__ float act_value(int act, float g) {
+  if (act == kActSilu) return g * sigmoid_f(g);
+  if (act == kActGelu) return 0.5f * g * erfcf(g * -0.70710678118654752f);
+  return g * sigmoid_f(kGeluC * (g + kGeluA * g * g * g));
+}
+
+// act(g) and act'(g)
+__device__ __forceinline__ void act_value_grad(int act, float g, float& a, float& da) {
+  if (act == kActSilu) {
+    const float s = sigmoid_f(g);
+    a = g * s;
+    da = s * (1.0f + g * (1.0f - s));
+  } else if (act == kActGelu) {
+    const float cdf = 0.5f * erfcf(g * -0.70710678118654752f);
+    a = g * cdf;
+    da = cdf + g * 0.39894228040143268f * __builtin_amdgcn_exp2f(g * g * -0.72134752044448170f);
+  } else {
+    const float s = sigmoid_f(kGeluC * (g + kGeluA * g * g * g));
+    a = g * s;
+    // s (1 - s) is 0 in binary32 beyond |g| = 10: the polynomial is held there
+    const float c = fminf(fmaxf(g, -10.0f), 10.0f);
+    da = s + c * s * (1.0f - s) * kGeluC * (1.0f + 3.0f * kGeluA * c * c);
+  }
+}
+
+// ---- one operand of a tile -------------------------------------------------
+// Position of 16-byte chunk c of row r inside its 128 bytes is c ^ tile_swz(r).
+__device__ __forceinline__ constexpr int tile_swz(int r) { return (r ^ ((r >> 3) & 3)) & 7; }
+
+// Transposed: pair of 32-byte units u / 2 of k row k is kept at (u / 2) ^
+// tile_tswz.  k rows of 256 bytes or more start at the same bank, those of 128
+// bytes (ROWS 64) alternate between two halves.
+template <int ROWS>
+__device__ __forceinline__ constexpr int tile_tswz(int k) { return ROWS == 64 ? (k >> 1) & 1 : k & 3; }
+
+// ROWS tile rows (m or n) of one operand, its 1 KB loads shared by WAVES waves
+// (load q = wave * kLoads + j).
+//   rows along K: load q holds tile rows 8q .. 8q + 7; lane l brings position
+//     l % 8 of row 8q + l / 8.  With kPairs the tile rows are blocks of 32
+//     alternating between two row ranges (gate and up), each its own buffer.
+//   transposed: load q holds 512 / ROWS k rows.
+template <int ROWS, bool kTrans, bool kPairs, int WAVES>
+struct TileLoader {
+  static constexpr int kBytes = ROWS * kTileStage;
+  static constexpr int kLoads = kBytes / 1024 / WAVES;
+  static_assert(kLoads * WAVES * 1024 == kBytes, "whole loads per wave");
+  static_assert(!(kTrans && kPairs), "a gated weight has its rows along K");
+
+  uint32_t off[kLoads];
+  uint32_t c16[kTrans ? 1 : kLoads];  // byte position of the lane's chunk in the row's 128
+  v4u32 rsrc[kPairs ? 2 : 1];
+  const uint8_t* base;  // transposed: tile's first column of k row 0
+  int64_t ld;
+  int cols;             // transposed: bytes left of the tile's first column
+  int q0;
+
+  // rows along K: `p` the first tile row (`p2` that of the second range), `rows`
+  // valid rows left.  transposed: `p` the operand, first column `first` of `rows`.
+  __device__ __forceinline__ void init(const uint8_t* p, const uint8_t* p2, int64_t ld_, int rows, int first, int wave,
+                                       int lane) {
+    q0 = wave * kLoads;
+    ld = ld_;
+    if constexpr (kTrans) {
+      base = p + (int64_t)first * 2;
+      cols = first * 2;
+      constexpr int kLanesRow = ROWS / 8;  // 16-byte pieces of a k row
+#pragma unroll
+      for (int j = 0; j < kLoads; j++) {
+        const int k = (q0 + j) * (64 / kLanesRow) + lane / kLanesRow;
+        const int pos = lane % kLanesRow;
+        const int col = (((pos >> 1) ^ (2 * tile_tswz<ROWS>(k))) * 16) + (pos & 1) * 8;
+        off[j] = first + col < rows ? (uint32_t)(k * ld + col * 2) : kBufOOB;
+      }
+    } else {
+      const int lim = min(rows, kPairs ? ROWS / 2 : ROWS);
+      rsrc[0] = make_rsrc4(p, (int64_t)lim * ld);
+      if constexpr (kPairs) rsrc[1] = make_rsrc4(p2, (int64_t)lim * ld);
+#pragma unroll
+      for (int j = 0; j < kLoads; j++) {
+        const int q = q0 + j, r = 8 * q + lane / 8;
+        const int row = kPairs ? (q >> 3) * 32 + (r & 31) : r;
+        c16[j] = (uint32_t)((lane & 7) ^ tile_swz(r)) * 16;
+        off[j] = row < lim ? (uint32_t)(row * ld) + c16[j] : kBufOOB;
+      }
+    }
+  }
+
+  // Stage `st` (of kb bytes of K, or k rows) into LDS at `lds`.
+  __device__ __forceinline__ void issue(int st, int64_t kend, uint32_t lds) const {
+    if constexpr (kTrans) {
+      const int64_t k = (int64_t)st * kTileStageK;
+      const int left = (int)min((int64_t)kTileStageK, kend - k);
+      const v4u32 r = make_rsrc4(base + k * ld, (int64_t)left * ld - cols);
+#pragma unroll
+      for (int j = 0; j < kLoads; j++) buf_lds16(r, off[j], 0, lds + (uint32_t)(q0 + j) * 1024);
+    } else {
+      const uint32_t soff = (uint32_t)st * kTileStage;
+      const int left = (int)min((int64_t)kTileStage, kend - (int64_t)soff);
+#pragma unroll
+      for (int j = 0; j < kLoads; j++) {
+        const v4u32 r = kPairs && (((q0 + j) >> 2) & 1) ? rsrc[kPairs ? 1 : 0] : rsrc[0];
+        const uint32_t v = (int)c16[j] < left ? off[j] : kBufOOB;
+        buf_lds16(r, v, soff, lds + (uint32_t)(q0 + j) * 1024);
+      }
+    }
+  }
+};
+
+// Fragments of 32-row blocks from a stage in LDS: 16 bytes per lane, K chunk
+// 2 kk + lane / 32 of row lane % 32.
+template <int ROWS, bool kTrans, int T>
+struct TileReader {
+  uint32_t off[kTrans ? T : 4];  // LDS byte offsets inside the operand's stage
+  __device__ __forceinline__ void init(int block0, int lane) {
+    if constexpr (kTrans) {
+      const int s = (lane & 15) >> 2;
+#pragma unroll
+      for (int i = 0; i < T; i++)
+        off[i] = (uint32_t)((8 * (lane >> 5) + s) * ROWS * 2 + (2 * ((block0 + i) ^ tile_tswz<ROWS>(s)) + ((lane >> 4) & 1)) * 32 +
+                            (lane & 3) * 8);
+    } else {
+      const int lr = lane & 31;
+#pragma unroll
+      for (int kk = 0; kk < 4; kk++)
+        off[kk] = (uint32_t)((block0 * 32 + lr) * kTileStage + (((2 * kk + (lane >> 5)) ^ tile_swz(lr)) * 16));
+    }
+  }
+  __device__ __forceinline__ v4i read(const uint8_t* stage, int i, int kk) const {
+    if constexpr (kTrans) {
+      typedef short v4s __attribute__((ext_vector_type(4)));
+      typedef __attribute__((address_space(3))) v4s lds_v4s;
+      lds_v4s* p = (lds_v4s*)(const __attribute__((address_space(3))) uint8_t*)(stage + off[i] + kk * 16 * ROWS * 2);
+      const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(p);
+      const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(p + ROWS);  // four k rows on (8 bytes per element)
+      const uint2 a = __builtin_bit_cast(uint2, lo), b = __builtin_bit_cast(uint2, hi);
+      return v4i{(int)a.x, (int)a.y, (int)b.x, (int)b.y};
+    } else {
+      return *reinterpret_cast<const v4i*>(stage + off[kk] + i * 32 * kTileStage);
+    }
+  }
+};
+
+// ---- the kernel ------------------------------------------------------------
+constexpr int kTileStore = 0;  // D = bf16 rows (scales and bias for 8-bit operands)
+constexpr int kTileGated = 1;  // columns are gate / up pairs: act(gate) * up
+
+struct TileArgs {
+  const uint8_t* A;
+  const uint8_t* B;
+  int64_t lda, ldb;    // bytes from one stored row to the next
+  int M;               // output rows
+  int N;               // output columns (gated: of h; B holds N gate rows, then N up rows)
+  int64_t kend;        // K in bytes (both operands along K) or in k rows (any transposed)
+  const float* sa;     // 8-bit: scale per row of A
+  const float* sb;     // 8-bit: scale per row of B
+  const uint16_t* bias;  // [N] or null (store)
+  uint16_t* D;         // [M, N]
+  uint16_t* gate_up;   // gated: bf16 [M, 2 N] or null
+  int act;
+  int tiles_m, tiles_n, splits;
+  void* part;          // splits > 1: float / int32 [splits][M][N or 2 N]
+};
+
+template <int BM, int BN>
+constexpr int tile_smem() {
+  const int ring = 2 * (BM + BN) * kTileStage;
+  const int out = BM * (BN * 2 + 16);
+  return ring > out ? ring : out;
+}
+
+// Waves per SIMD that the LDS lets in: what the registers are sized for.
+template <int BM, int BN, int WAVES>
+constexpr int tile_waves_simd() {
+  const int w = 160 * 1024 / tile_smem<BM, BN>() * WAVES / 4;
+  return w < 1 ? 1 : w;
+}
+
+// Work item of a workgroup.  Workgroups are dispatched round-robin over the 8
+// XCDs; consecutive items go to one XCD and run down bands of `band` tile rows, so
+// an XCD's items share few A and B panels in its L2.
+__device__ __forceinline__ void tile_item(const TileArgs& p, int& tile_m, int& tile_n, int& split) {
+  const int items = p.tiles_m * p.tiles_n * p.splits;
+  // the first 8 * (items / 8) workgroups are remapped, the rest keep their index
+  const int per = items / 8;
+  int item = blockIdx.x;
+  if (item < per * 8) item = (item % 8) * per + item / 8;
+  split = item % p.splits;
+  const int tile = item / p.splits;
+  constexpr int kBand = 4;
+  const int band_tiles = kBand * p.tiles_n;
+  const int band = tile / band_tiles, in_band = tile % band_tiles;
+  const int rows = min(kBand, p.tiles_m - band * kBand);
+  tile_m = band * kBand + in_band % rows;
+  tile_n = in_band / rows;
+}
+
+template <bool kInt8, int BM, int BN, int WGM, int WGN, bool kTransA, bool kTransB, int EPI>
+__global__ void __launch_bounds__(64 * WGM * WGN, (tile_waves_simd<BM, BN, WGM * WGN>()))
+    tile_gemm(const TileArgs p) {
+  typedef Mma<kInt8> MM;
+  constexpr int NT = 64 * WGM * WGN, WAVES = WGM * WGN;
+  constexpr int WM = BM / WGM, WN = BN / WGN, TM = WM / 32, TN = WN / 32;
+  constexpr int kStageA = BM * kTileStage, kStage = (BM + BN) * kTileStage;
+  constexpr bool kGated = EPI == kTileGated;
+  static_assert(!kGated || TN % 2 == 0, "a wave holds gate / up block pairs");
+  static_assert(!kInt8 || (!kTransA && !kTransB), "8-bit operands have their rows along K");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[tile_smem<BM, BN>()];
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WGN, wn = wave % WGN, g = lane >> 5, lr = lane & 31;
+  int tile_m, tile_n, split;
+  tile_item(p, tile_m, tile_n, split);
+  constexpr int kCols = kGated ? BN / 2 : BN;  // output columns of a tile
+  const int m0 = tile_m * BM, n0 = tile_n * kCols;
+
+  constexpr int64_t kStep = (kTransA || kTransB) ? kTileStageK : kTileStage;
+  const int total = (int)((p.kend + kStep - 1) / kStep);
+  const int s0 = (int)((int64_t)total * split / p.splits), s1 = (int)((int64_t)total * (split + 1) / p.splits);
+
+  TileLoader<BM, kTransA, false, WAVES> la;
+  TileLoader<BN, kTransB, kGated, WAVES> lb;
+  if constexpr (kTransA) la.init(p.A, nullptr, p.lda, p.M, m0, wave, lane);
+  else la.init(p.A + (int64_t)m0 * p.lda, nullptr, p.lda, p.M - m0, 0, wave, lane);
+  if constexpr (kTransB) lb.init(p.B, nullptr, p.ldb, p.N, n0, wave, lane);
+  else lb.init(p.B + (int64_t)n0 * p.ldb, p.B + ((int64_t)p.N + n0) * p.ldb, p.ldb, p.N - n0, 0, wave, lane);
+  // an operand along K beside a transposed one: K counted in bytes there
+  const int64_t kend_a = !kTransA && kTransB ? p.kend * 2 : p.kend;
+  const int64_t kend_b = !kTransB && kTransA ? p.kend * 2 : p.kend;
+  TileReader<BM, kTransA, TM> ra;
+  TileReader<BN, kTransB, TN> rb;
+  ra.init(wm * TM, lane);
+  rb.init(wn * TN, lane);
+  const uint32_t lds0 = lds_offset(smem);
+  auto issue = [&](int st) {
+    const uint32_t slot = lds0 + (uint32_t)(st & 1) * kStage;
+    la.issue(st, kend_a, slot);
+    lb.issue(st, kend_b, slot + kStageA);
+  };
+
+  typename MM::Acc acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; i++)
+#pragma unroll
+    for (int j = 0; j < TN; j++) acc[i][j] = typename MM::Acc{};
+
+  if (s0 < s1) issue(s0);
+  for (int st = s0; st < s1; st++) {
+    wait_vmcnt<0>();  // this wave's loads of stage st
+    __builtin_amdgcn_s_barrier();  // everyone's; and everyone is done with the other slot
+    asm volatile("" ::: "memory");
+    if (st + 1 < s1) issue(st + 1);
+    const uint8_t* qa = smem + (st & 1) * kStage;
+    const uint8_t* qb = qa + kStageA;
+    v4i fa[2][TM], fb[2][TN];
+#pragma unroll
+    for (int j = 0; j < TN; j++) fb[0][j] = rb.read(qb, j, 0);
+#pragma unroll
+    for (int i = 0; i < TM; i++) fa[0][i] = ra.read(qa, i, 0);
+#pragma unroll
+    for (int kk = 0; kk < 4; kk++) {
+      if (kk < 3) {
+#pragma unroll
+        for (int j = 0; j < TN; j++) fb[(kk + 1) & 1][j] = rb.read(qb, j, kk + 1);
+#pragma unroll
+        for (int i = 0; i < TM; i++) fa[(kk + 1) & 1][i] = ra.read(qa, i, kk + 1);
+      }
+      // the B fragment as first operand: a lane ends with four consecutive
+      // columns of one row in each register quad
+#pragma unroll
+      for (int i = 0; i < TM; i++)
+#pragma unroll
+        for (int j = 0; j < TN; j++) acc[i][j] = MM::run(fb[kk & 1][j], fa[kk & 1][i], acc[i][j]);
+    }
+    asm volatile("" ::: "memory");
+  }
+
+  // register 4q + e of block (i, j): row wm*WM + 32 i + lr, tile column wn*WN + 32 j + 8q + 4g + e
+  if (p.splits > 1) {
+    const int64_t width = kGated ? 2 * (int64_t)p.N : p.N;
+    float* dst = reinterpret_cast<float*>(p.part) + (int64_t)split * p.M * width;
+#pragma unroll
+    for (int i = 0; i < TM; i++) {
+      const int m = m0 + wm * WM + i * 32 + lr;
+      if (m >= p.M) continue;
+#pragma unroll
+      for (int j = 0; j < TN; j++)
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+          const int n = n0 + (kGated ? wn * (WN / 2) + (j / 2) * 32 : wn * WN + j * 32) + 8 * q + 4 * g;
+          if (n >= p.N) continue;
+          typedef typename std::conditional<kInt8, int, float>::type T;
+          const T v[4] = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+          *reinterpret_cast<uint4*>(dst + (int64_t)m * width + (kGated && (j & 1) ? p.N : 0) + n) =
+              make_uint4(__builtin_bit_cast(uint32_t, v[0]), __builtin_bit_cast(uint32_t, v[1]),
+                         __builtin_bit_cast(uint32_t, v[2]), __builtin_bit_cast(uint32_t, v[3]));
+        }
+    }
+    return;
+  }
+
+  // bf16 through LDS: each lane's four-column runs into a row-major tile, then
+  // whole 16-byte row segments per lane to memory
+  constexpr int kPitch = kCols * 2 + 16;
+  __syncthreads();  // the stages are done with
+  auto flush = [&](uint16_t* dst, int64_t pitch) {
+    __syncthreads();
+    constexpr int kChunksRow = kCols / 8;
+    for (int idx = tid; idx < BM * kChunksRow; idx += NT) {
+      const int r = idx / kChunksRow, c = (idx % kChunksRow) * 8;
+      if (m0 + r < p.M && n0 + c < p.N)
+        *reinterpret_cast<uint4*>(dst + (int64_t)(m0 + r) * pitch + n0 + c) =
+            *reinterpret_cast<const uint4*>(smem + r * kPitch + c * 2);
+    }
+  };
+  float sa[TM];
+#pragma unroll
+  for (int i = 0; i < TM; i++) {
+    const int m = m0 + wm * WM + i * 32 + lr;
+    sa[i] = kInt8 && m < p.M ? p.sa[m] : 0.0f;
+  }
+  auto quad = [&](int i, int j, int q, const float4& sb) -> float4 {
+    const auto& a = acc[i][j];
+    if constexpr (kInt8)
+      return make_float4((float)a[4 * q] * sa[i] * sb.x, (float)a[4 * q + 1] * sa[i] * sb.y,
+                         (float)a[4 * q + 2] * sa[i] * sb.z, (float)a[4 * q + 3] * sa[i] * sb.w);
+    else
+      return make_float4(a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]);
+  };
+  auto scales = [&](int n) -> float4 {  // of B rows n .. n + 3
+    if constexpr (kInt8) return *reinterpret_cast<const float4*>(p.sb + n);
+    else return make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+  };
+  if constexpr (!kGated) {
+#pragma unroll
+    for (int j = 0; j < TN; j++)
+#pragma unroll
+      for (int q = 0; q < 4; q++) {
+        const int c = wn * WN + j * 32 + 8 * q + 4 * g, n = min(n0 + c, p.N - 4);
+        const float4 sb = scales(n);
+        float4 bv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (kInt8 && p.bias) {
+          const uint2 b = *reinterpret_cast<const uint2*>(p.bias + n);
+          bv = make_float4(bf16_lo(b.x), bf16_hi(b.x), bf16_lo(b.y), bf16_hi(b.y));
+        }
+#pragma unroll
+        for (int i = 0; i < TM; i++) {
+          float4 v = quad(i, j, q, sb);
+          if (kInt8) v = make_float4(v.x + bv.x, v.y + bv.y, v.z + bv.z, v.w + bv.w);
+          *reinterpret_cast<uint2*>(smem + (wm * WM + i * 32 + lr) * kPitch + c * 2) =
+              make_uint2(pack_bf16x2_ieee(v.x, v.y), pack_bf16x2_ieee(v.z, v.w));
+        }
+      }
+    flush(p.D, p.N);
+  } else {
+    // pass 0: h = act(gate) * up; with gate_up, pass 1: gate, pass 2: up
+    const int passes = p.gate_up ? 3 : 1;
+    for (int pass = 0; pass < passes; pass++) {
+      if (pass > 0) __syncthreads();
+#pragma unroll
+      for (int j = 0; j < TN; j += 2)
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+          const int c = wn * (WN / 2) + (j / 2) * 32 + 8 * q + 4 * g, n = min(n0 + c, p.N - 4);
+          const float4 sg = scales(n), su = scales(p.N + n);
+#pragma unroll
+          for (int i = 0; i < TM; i++) {
+            const float4 gv = quad(i, j, q, sg), uv = quad(i, j + 1, q, su);
+            float4 v;
+            if (pass == 0)
+              v = make_float4(act_value(p.act, gv.x) * uv.x, act_value(p.act, gv.y) * uv.y,
+                              act_value(p.act, gv.z) * uv.z, act_value(p.act, gv.w) * uv.w);
+            else
+              v = pass == 1 ? gv : uv;
+            *reinterpret_cast<uint2*>(smem + (wm * WM + i * 32 + lr) * kPitch + c * 2) =
+                make_uint2(pack_bf16x2_ieee(v.x, v.y), pack_bf16x2_ieee(v.z, v.w));
+          }
+        }
+      if (pass == 0) flush(p.D, p.N);
+      else flush(p.gate_up + (pass == 1 ? 0 : p.N), 2 * (int64_t)p.N);
+    }
+  }
+}
+
+// ---- split K ---------------------------------------------------------------
+// Sums the splits' partials in split order (8-bit: exact integers) and finishes
+// the rows as the tile's epilogue would.  One thread: eight output columns.
+template <bool kInt8, int EPI>
+__global__ void __launch_bounds__(256)
+    tile_reduce(const TileArgs p) {
+  typedef typename std::conditional<kInt8, int, float>::type T;
+  constexpr bool kGated = EPI == kTileGated;
+  const int64_t width = kGated ? 2 * (int64_t)p.N : p.N;
+  const int64_t mn = (int64_t)p.M * width;
+  const int64_t chunks = p.N / 8, all = (int64_t)p.M * chunks;
+  const int64_t stride = (int64_t)gridDim.x * blockDim.x;
+  for (int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; idx < all; idx += stride) {
+    const int64_t m = idx / chunks;
+    const int n = (int)(idx - m * chunks) * 8;
+    auto sum8 = [&](int64_t col, const float* sb, float (&v)[8]) {
+      const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p.part) + m * width + col);
+      T t[8] = {};
+#pragma unroll 4
+      for (int s = 0; s < p.splits; s++) {
+        const uint4 a = src[s * (mn / 4)], b = src[s * (mn / 4) + 1];
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int k = 0; k < 8; k++) t[k] += __builtin_bit_cast(T, w[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; k++) v[k] = kInt8 ? (float)t[k] * p.sa[m] * sb[col + k] : (float)t[k];
+    };
+    float v[8];
+    sum8(n, p.sb, v);
+    if constexpr (kGated) {
+      float u[8];
+      sum8(p.N + n, p.sb, u);
+      if (p.gate_up) {
+        *reinterpret_cast<uint4*>(p.gate_up + m * width + n) = pack8(v);
+        *reinterpret_cast<uint4*>(p.gate_up + m * width + p.N + n) = pack8(u);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; k++) v[k] = act_value(p.act, v[k]) * u[k];
+    } else if (kInt8 && p.bias) {
+      float b[8];
+      unpack8(*reinterpret_cast<const uint4*>(p.bias + n), b);
+#pragma unroll
+      for (int k = 0; k < 8; k++) v[k] += b[k];
+    }
+    *reinterpret_cast<uint4*>(p.D + m * (int64_t)p.N + n) = pack8(v);
+  }
+}
+
+// ---- planning --------------------------------------------------------------
+struct TilePlan {
+  int bm, bn, splits;
+};
+
+// Tile shape and K split of an M x N (x K bytes) product: the shape whose
+// estimated time is least.  Time = rounds of workgroups x (bytes of K per split /
+// measured bytes of K a workgroup takes per second) + a fixed part per round +
+// the partials' traffic and the second launch of a split.  N counts weight rows
+// (gated: both halves).
+inline TilePlan plan_tile(int64_t M, int64_t N, int64_t kbytes, int cus) {
+  struct Cand {
+    int bm, bn, per_cu;
+    double us_stage;  // microseconds a stage of 128 bytes takes a workgroup, the CU full
+  };
+  static constexpr Cand cands[] = {{256, 256, 1, 1.0}, {128, 128, 2, 0.55}, {64, 128, 3, 0.45}};
+  const int64_t stages = (kbytes + kTileStage - 1) / kTileStage;
+  TilePlan best{256, 256, 1};
+  double best_t = 1e300;
+  for (const Cand& c : cands) {
+    const int64_t tiles = ((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
+    for (int sp = 1; sp <= 16; sp++) {
+      if (sp > 1 && stages / sp < 4) break;
+      const int64_t slots = (int64_t)cus * c.per_cu;
+      const int64_t rounds = (tiles * sp + slots - 1) / slots;
+      double t = rounds * ((double)((stages + sp - 1) / sp) * c.us_stage + 2.0);
+      if (sp > 1) t += 2.0 * sp * M * N * 4 / 5.0e6 + 3.0;
+      if (t < best_t * 0.999) {
+        best_t = t;
+        best = TilePlan{c.bm, c.bn, sp};
+      }
+    }
+  }
+  return best;
+}
+
+inline size_t tile_workspace(const TilePlan& pl, int64_t M, int64_t N) {
+  return pl.splits > 1 ? (size_t)pl.splits * M * N * 4 : 0;
+}
+
+template <bool kInt8, bool kTransA, bool kTransB, int EPI>
+hipError_t launch_tile(TileArgs a, const TilePlan& pl, hipStream_t stream) {
+  const int64_t brows = EPI == kTileGated ? 2 * (int64_t)a.N : a.N;
+  a.tiles_m = (int)((a.M + pl.bm - 1) / pl.bm);
+  a.tiles_n = (int)((brows + pl.bn - 1) / pl.bn);
+  a.splits = pl.splits;
+  const unsigned grid = (unsigned)((int64_t)a.tiles_m * a.tiles_n * a.splits);
+  if (pl.bm == 256)
+    tile_gemm<kInt8, 256, 256, 2, 4, kTransA, kTransB, EPI><<<grid, 512, 0, stream>>>(a);
+  else if (pl.bm == 128)
+    tile_gemm<kInt8, 128, 128, 2, 2, kTransA, kTransB, EPI><<<grid, 256, 0, stream>>>(a);
+  else
+    tile_gemm<kInt8, 64, 128, 2, 2, kTransA, kTransB, EPI><<<grid, 256, 0, stream>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  const int64_t items = (int64_t)a.M * (a.N / 8);
+  tile_reduce<kInt8, EPI><<<(unsigned)std::min<int64_t>((items + 255) / 256, 8192), 256, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace bsfp4

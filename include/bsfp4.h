@@ -20,6 +20,8 @@
  *   E8M0   8-bit power-of-two scale 2^(c-127); one per 32 K-elements in the
  *          MXFP4 form ("[Kernel] Enable CUTLASS MXFP4 W4A4 MoE on SM12x").
  *   bf16   activations and outputs, passed as 16-bit patterns.
+ *   int8   8-bit integers with one FP32 scale per row (token or output
+ *          channel), value q * s, one byte per element.
  * Scale tensors are row-major [rows, K/16] (NVFP4) or [rows, K/32] (MXFP4),
  * one byte per block, unpadded and unswizzled.  Codes are row-major
  * [rows, K/2].  Every matrix is contiguous.
@@ -390,6 +392,156 @@ BSFP4_API bsfp4_status nvfp4_moe_grouped_gemm(const uint8_t* Aq, const uint8_t* 
                                               const float* alpha_experts, int64_t N, int64_t K,
                                               int epilogue, const bsfp4_moe_epilogue_args* ep, void* ws,
                                               size_t ws_bytes, void* stream);
+
+/* ----------------------------------------------------------------------------
+ * 8-bit integer products: the projections of a model that are kept at 8 bits
+ * beside its FP4 ones, with one scale per token and one per output channel.
+ *
+ * bsfp4_int8_quantize: bf16 rows -> 8-bit rows.  Per row, amax = max |x|:
+ *   s = fl32(amax / 127),  q = round-to-nearest-even of 127 x / amax (the exact
+ *   quotient; |q| <= 127)
+ *   A row of zeros gives s = 0 and q = 0.  A row with an infinity or a NaN
+ *   gives s = NaN and q = 0, so every result computed from it is NaN.
+ *   x    device bf16 [M, K], M >= 0, K > 0, K % 8 == 0 (the products below
+ *        take K % 16 == 0)
+ *   q    device int8 [M, K]
+ *   s    device float [M]
+ *
+ * bsfp4_int8_gemm: D[M,N] = bf16_rne(acc * sa[m] * sb[n] + bias[n]),
+ *   acc = sum_k A[m,k] * B[n,k], an exact 32-bit integer; acc -> FP32, the two
+ *   scale products and the bias sum are one FP32 rounding each.
+ *   A, sa    device int8 [M, K], float [M]
+ *   B, sb    device int8 [N, K], float [N] (any values, -128 included)
+ *   bias     device bf16 [N] or NULL
+ *   D        device bf16 [M, N]
+ *   sizes    M >= 0, N > 0, N % 8 == 0, K > 0, K % 16 == 0, K <= 131056 (the
+ *            integer sum stays below 2^31)
+ *   ws       device workspace of bsfp4_int8_gemm_workspace_size(M, N, K) bytes
+ *            (may be NULL when that is 0); needs no initialisation
+ *
+ * bsfp4_int8_quantize_gemm: bsfp4_int8_gemm(bsfp4_int8_quantize(x), B) in one
+ *   call, bit for bit the output of the two.
+ *   ws       bsfp4_int8_quantize_gemm_workspace_size(M, N, K) bytes
+ *
+ * bsfp4_int8_gated_ffn: h[M,I] = bf16_rne(act(G) * U) with [G | U] the scaled
+ *   product of A and W in FP32 (not rounded in between).
+ *   W, sw    device int8 [2 I, K], float [2 I]: gate rows, then up rows
+ *   act      one of bsfp4_activation
+ *   h        device bf16 [M, I], I > 0, I % 8 == 0
+ *   ws       bsfp4_int8_gated_ffn_workspace_size(M, I, K) bytes
+ * ------------------------------------------------------------------------- */
+typedef enum bsfp4_activation {
+  BSFP4_ACT_SILU = 0,     /* v * sigmoid(v) */
+  BSFP4_ACT_GELU = 1,     /* v * Phi(v), the normal distribution function */
+  BSFP4_ACT_GELU_TANH = 2 /* 0.5 v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) */
+} bsfp4_activation;
+
+BSFP4_API bsfp4_status bsfp4_int8_quantize(const uint16_t* x, int64_t M, int64_t K, int8_t* q, float* s,
+                                           void* stream);
+BSFP4_API size_t bsfp4_int8_gemm_workspace_size(int64_t M, int64_t N, int64_t K);
+BSFP4_API bsfp4_status bsfp4_int8_gemm(const int8_t* A, const float* sa, const int8_t* B, const float* sb,
+                                       const uint16_t* bias, uint16_t* D, int64_t M, int64_t N, int64_t K,
+                                       void* ws, size_t ws_bytes, void* stream);
+BSFP4_API size_t bsfp4_int8_quantize_gemm_workspace_size(int64_t M, int64_t N, int64_t K);
+BSFP4_API bsfp4_status bsfp4_int8_quantize_gemm(const uint16_t* x, const int8_t* B, const float* sb,
+                                                const uint16_t* bias, uint16_t* D, int64_t M, int64_t N,
+                                                int64_t K, void* ws, size_t ws_bytes, void* stream);
+BSFP4_API size_t bsfp4_int8_gated_ffn_workspace_size(int64_t M, int64_t I, int64_t K);
+BSFP4_API bsfp4_status bsfp4_int8_gated_ffn(const int8_t* A, const float* sa, const int8_t* W, const float* sw,
+                                            int act, uint16_t* h, int64_t M, int64_t I, int64_t K, void* ws,
+                                            size_t ws_bytes, void* stream);
+
+/* ----------------------------------------------------------------------------
+ * Gated feed-forward product in bf16 (a model's dense or shared-expert layer
+ * beside its FP4 experts), forward and backward.
+ *
+ * bsfp4_gated_ffn: [G | U] = x W^T (FP32 sums), h = bf16_rne(act(G) * U).
+ *   x        device bf16 [M, H], M >= 0
+ *   W        device bf16 [2 I, H]: gate rows, then up rows
+ *   h        device bf16 [M, I]
+ *   gate_up  device bf16 [M, 2 I] or NULL: [G | U] rounded, for the backward
+ *            pass
+ *   sizes    H > 0, I > 0, multiples of 8, H < 2^22, I < 2^21
+ *   ws       bsfp4_gated_ffn_workspace_size(M, I, H) bytes
+ *
+ * bsfp4_gated_ffn_backward: from dh = dL/dh, with dG = dh U act'(G) and dU =
+ *   dh act(G) (FP32 from gate_up, rounded to bf16 for the matrix cores):
+ *     dx = bf16_rne([dG | dU] W),  dW = bf16_rne([dG | dU]^T x)
+ *   dx       device bf16 [M, H] or NULL (not computed)
+ *   dW       device bf16 [2 I, H] or NULL (not computed); zeros for M == 0
+ *   ws       bsfp4_gated_ffn_backward_workspace_size(M, I, H) bytes
+ * Every output is a sum in a fixed order: the same call gives the same bits.
+ * ------------------------------------------------------------------------- */
+BSFP4_API size_t bsfp4_gated_ffn_workspace_size(int64_t M, int64_t I, int64_t H);
+BSFP4_API bsfp4_status bsfp4_gated_ffn(const uint16_t* x, const uint16_t* W, int act, uint16_t* h,
+                                       uint16_t* gate_up, int64_t M, int64_t I, int64_t H, void* ws,
+                                       size_t ws_bytes, void* stream);
+BSFP4_API size_t bsfp4_gated_ffn_backward_workspace_size(int64_t M, int64_t I, int64_t H);
+BSFP4_API bsfp4_status bsfp4_gated_ffn_backward(const uint16_t* dh, const uint16_t* x, const uint16_t* W,
+                                                const uint16_t* gate_up, int act, uint16_t* dx, uint16_t* dW,
+                                                int64_t M, int64_t I, int64_t H, void* ws, size_t ws_bytes,
+                                                void* stream);
+
+/* ----------------------------------------------------------------------------
+ * Norms before and after a block, fused with the block's gate, the branch
+ * scale and the residual add: the producer of the quantisers' inputs.
+ *
+ * bsfp4_block_norm, per row of H values, rstd(v) = fl32(1/sqrt(mean(v^2) + eps)):
+ *     n       = x * rstd(x) * w_post               (n = x when w_post is NULL)
+ *     res_out = bf16_rne(residual + (gate * scale) * n)
+ *     z       = bf16_rne(res_out * rstd(res_out) * w_pre)
+ *   each step one FP32 operation in this order, the mean squares in FP64.
+ *   x          bf16 [T, H] or NULL: only the pre-norm of `residual` (w_pre
+ *              required; w_post and gate must be NULL, res_out is not written)
+ *   residual   bf16 [T, H]
+ *   w_post     bf16 [H] or NULL;  w_pre  bf16 [H] or NULL (no z)
+ *   gate       bf16 [groups, H] or NULL (1); rows [g T/groups, (g+1) T/groups)
+ *              use gate row g; T % groups == 0
+ *   res_out    bf16 [T, H]; may be `residual` or `x` itself
+ *   z          bf16 [T, H]; or NULL and, instead of it,
+ *   q, s       int8 [T, H], float [T]: bsfp4_int8_quantize of z
+ *   sizes      T >= 0, H > 0, H % 8 == 0, H <= 16384, groups >= 1, eps > 0
+ *
+ * bsfp4_block_norm_backward: gradients of the above (z in bf16) from dres_out
+ *   and dz.  Row sums and the vectors' gradients are FP32 or wider; the
+ *   gradient with respect to res_out is that of its unrounded value.
+ *   x, w_post, w_pre, gate, scale, eps, T, H, groups  as in the forward call
+ *   res_out    bf16 [T, H] as the forward call wrote it (x NULL: its
+ *              residual); required with w_pre
+ *   dres_out   bf16 [T, H] or NULL (zeros);  dz  bf16 [T, H], required with
+ *              w_pre, else NULL
+ *   dx, dres   bf16 [T, H]: gradients of x (required with x) and residual
+ *   dw_post, dw_pre  float [H]; dgate  float [groups, H]: required where the
+ *              vector is given, NULL elsewhere
+ *   ws         bsfp4_block_norm_backward_workspace_size(T, H, groups) bytes
+ * Vector gradients are summed in a fixed order (no atomics).
+ * ------------------------------------------------------------------------- */
+typedef struct bsfp4_block_norm_args {
+  const uint16_t* x;
+  const uint16_t* residual; /* forward */
+  const uint16_t* w_post;
+  const uint16_t* w_pre;
+  const uint16_t* gate;
+  double scale; /* rounded to FP32 */
+  double eps;
+  int64_t T, H, groups;
+  uint16_t* res_out; /* forward: written; backward: read */
+  uint16_t* z;       /* forward */
+  int8_t* q;         /* forward */
+  float* s;          /* forward */
+  const uint16_t* dres_out; /* backward, from here on */
+  const uint16_t* dz;
+  uint16_t* dx;
+  uint16_t* dres;
+  float* dw_post;
+  float* dw_pre;
+  float* dgate;
+} bsfp4_block_norm_args;
+
+BSFP4_API bsfp4_status bsfp4_block_norm(const bsfp4_block_norm_args* args, void* stream);
+BSFP4_API size_t bsfp4_block_norm_backward_workspace_size(int64_t T, int64_t H, int64_t groups);
+BSFP4_API bsfp4_status bsfp4_block_norm_backward(const bsfp4_block_norm_args* args, void* ws, size_t ws_bytes,
+                                                 void* stream);
 
 /* ----------------------------------------------------------------------------
  * Diagnostics.

@@ -1,0 +1,204 @@
+"""CPU: what the 8-bit, gated feed-forward and block-norm entry points refuse, in the binding (extents, types: meta
+tensors, nothing reaches the library) and in the C ABI (no kernel is launched: every call fails validation)."""
+import ctypes
+
+import pytest
+import torch
+
+import block_scaled_fp4_e2m1_amd as bs
+from block_scaled_fp4_e2m1_amd import binding
+
+I8, BF16, F32 = torch.int8, torch.bfloat16, torch.float32
+OK, INVALID, SHAPE, ALIGN, WORKSPACE = 0, 1, 2, 3, 4
+FAKE = 0x100000
+
+
+def m(*shape, dtype=BF16):
+    return torch.empty(shape, dtype=dtype, device="meta")
+
+
+def reaches_device_check(fn, *a, **kw):
+    with pytest.raises(ValueError, match="must be a device tensor"):
+        fn(*a, **kw)
+
+
+def refused(match, fn, *a, error=ValueError, **kw):
+    with pytest.raises(error, match=match):
+        fn(*a, **kw)
+
+
+def test_int8_quantize():
+    reaches_device_check(bs.int8_quantize, m(4, 64))
+    reaches_device_check(bs.int8_quantize, m(4, 64), q=m(4, 64, dtype=I8), s=m(4, dtype=F32))
+    refused("multiple of 8", bs.int8_quantize, m(4, 60))
+    refused("2-D", bs.int8_quantize, m(64))
+    refused("contiguous", bs.int8_quantize, m(64, 4).t())
+    refused("bfloat16", bs.int8_quantize, m(4, 64, dtype=F32), error=TypeError)
+    refused("q must have shape", bs.int8_quantize, m(4, 64), q=m(4, 56, dtype=I8))
+    refused("s must have shape", bs.int8_quantize, m(4, 64), s=m(5, dtype=F32))
+
+
+def test_int8_gemm():
+    A, SA, B, SB = m(4, 64, dtype=I8), m(4, dtype=F32), m(24, 64, dtype=I8), m(24, dtype=F32)
+    f = bs.int8_gemm
+    reaches_device_check(f, A, SA, B, SB)
+    reaches_device_check(f, A, SA, B, SB, bias=m(24), out=m(4, 24))
+    refused("K=64 but B has K=80", f, A, SA, m(24, 80, dtype=I8), SB)
+    refused("multiple of 16", f, m(4, 72, dtype=I8), SA, m(24, 72, dtype=I8), SB)
+    refused("N=20", f, A, SA, m(20, 64, dtype=I8), m(20, dtype=F32))
+    refused("SA must have", f, A, m(5, dtype=F32), B, SB)
+    refused("SB must have", f, A, SA, B, m(23, dtype=F32))
+    refused("bias must have", f, A, SA, B, SB, bias=m(23))
+    refused("out must have", f, A, SA, B, SB, out=m(4, 16))
+    refused("bfloat16", f, A, SA, B, SB, bias=m(24, dtype=F32), error=TypeError)
+    refused("int8", f, m(4, 64), SA, B, SB, error=TypeError)
+    g = bs.int8_quantize_gemm
+    reaches_device_check(g, m(4, 64), B, SB)
+    refused("K=80 but B has K=64", g, m(4, 80), B, SB)
+    refused("out must have", g, m(4, 64), B, SB, out=m(5, 24))
+
+
+def test_gated():
+    A, SA, W, SW = m(4, 64, dtype=I8), m(4, dtype=F32), m(32, 64, dtype=I8), m(32, dtype=F32)
+    reaches_device_check(bs.int8_gated_ffn, A, SA, W, SW, act="gelu")
+    refused("unknown activation", bs.int8_gated_ffn, A, SA, W, SW, act="relu")
+    refused("as many up rows", bs.int8_gated_ffn, A, SA, m(33, 64, dtype=I8), m(33, dtype=F32))
+    refused("I=12", bs.int8_gated_ffn, A, SA, m(24, 64, dtype=I8), m(24, dtype=F32))
+    refused("SW13 must have", bs.int8_gated_ffn, A, SA, W, m(16, dtype=F32))
+    refused("out must have", bs.int8_gated_ffn, A, SA, W, SW, out=m(4, 32))
+    x, W = m(4, 64), m(32, 64)
+    reaches_device_check(bs.gated_ffn, x, W, act="gelu_tanh", save_gate_up=True)
+    refused("W13 has H=56", bs.gated_ffn, x, m(32, 56))
+    refused("H=60", bs.gated_ffn, m(4, 60), m(32, 60))
+    refused("unknown activation", bs.gated_ffn, x, W, act=None)
+    refused("unknown activation", bs.gated_ffn, x, W, act=["silu"])
+    refused("out must have", bs.gated_ffn, x, W, out=m(4, 32))
+    dh, gu = m(4, 16), m(4, 32)
+    reaches_device_check(bs.gated_ffn_backward, dh, x, W, gu)
+    refused("dh must have", bs.gated_ffn_backward, m(4, 32), x, W, gu)
+    refused("gate_up must have", bs.gated_ffn_backward, dh, x, W, m(4, 16))
+    refused("contiguous", bs.gated_ffn_backward, dh, x, W, m(32, 4).t())
+
+
+def test_block_norm():
+    x, r, w = m(6, 64), m(6, 64), m(64)
+    f = bs.block_norm
+    reaches_device_check(f, x, r, w_post=w, w_pre=w, gate=m(3, 64))
+    reaches_device_check(f, None, r, w_pre=w, fmt="int8")
+    reaches_device_check(f, x, r, gate=w)
+    refused("x must have", f, m(6, 56), r)
+    refused("H=60", f, None, m(6, 60), w_pre=m(60))
+    refused("w_post must have", f, x, r, w_post=m(56))
+    refused("w_pre must have", f, x, r, w_pre=m(1, 64))
+    refused("gate must have", f, x, r, gate=m(3, 56))
+    refused("gate must have", f, x, r, gate=m(1, 3, 64))
+    refused("not a multiple of the 4", f, x, r, gate=m(4, 64))
+    refused("not a multiple of the 0", f, x, r, gate=m(0, 64))
+    refused("without x", f, None, r, w_post=w, w_pre=w)
+    refused("without x", f, None, r, w_pre=w, gate=w)
+    refused("nothing is written", f, None, r, w_pre=w, res_out=m(6, 64))
+    refused("neither x nor w_pre", f, None, r)
+    refused("unknown output format", f, x, r, w_pre=w, fmt="nvfp4")
+    refused("needs w_pre", f, x, r, fmt="int8")
+    refused("eps", f, x, r, eps=0.0)
+    refused("eps", f, x, r, eps=float("nan"))
+    refused("bfloat16", f, x, r, w_pre=m(64, dtype=F32), error=TypeError)
+    b = bs.block_norm_backward
+    reaches_device_check(b, r, r, x, r, w_post=w, w_pre=w, gate=w)
+    reaches_device_check(b, None, r, None, r, w_pre=w)
+    refused("w_pre needs", b, r, None, x, r, w_pre=w)
+    refused("w_pre needs", b, r, r, x, None, w_pre=w)
+    refused("dz without", b, r, r, x, r)
+    refused("dres is needed", b, None, None, x, r)
+    refused("dz must have", b, r, m(5, 64), x, r, w_pre=w)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return binding.load()
+
+
+def err(lib):
+    return lib.bsfp4_last_error().decode()
+
+
+def test_abi_int8(lib):
+    f = lib.bsfp4_int8_quantize
+    assert f(FAKE, 2, 20, FAKE, FAKE, None) == SHAPE and "multiple of 8" in err(lib)
+    assert f(FAKE, -1, 16, FAKE, FAKE, None) == SHAPE
+    assert f(None, 2, 16, FAKE, FAKE, None) == INVALID
+    assert f(FAKE + 8, 2, 16, FAKE, FAKE, None) == ALIGN
+    assert f(FAKE, 2, 16, FAKE, FAKE + 2, None) == ALIGN
+    assert f(None, 0, 16, None, None, None) == OK
+    g = lib.bsfp4_int8_gemm
+
+    def call(A=FAKE, sa=FAKE, B=FAKE, sb=FAKE, bias=None, D=FAKE, M=2, N=64, K=64, ws=None, n=0):
+        return g(A, sa, B, sb, bias, D, M, N, K, ws, n, None)
+
+    assert call(N=60) == SHAPE and "multiple of 8" in err(lib)
+    assert call(K=72) == SHAPE and "multiple of 16" in err(lib)
+    assert call(K=131072) == SHAPE and "131056" in err(lib)
+    assert call(M=1 << 31) == SHAPE
+    assert call(M=(1 << 31) - 1, N=1 << 20) == SHAPE and "2^40" in err(lib)
+    assert call(A=None) == INVALID and call(sb=None) == INVALID and call(D=None) == INVALID
+    assert call(sb=FAKE + 4) == ALIGN and call(bias=FAKE + 8) == ALIGN
+    assert call(M=0, A=None, sa=None, D=None) == OK
+    need = lib.bsfp4_int8_quantize_gemm_workspace_size(100, 64, 64)
+    assert need >= 100 * 64 + 400
+    h = lib.bsfp4_int8_quantize_gemm
+    assert h(FAKE, FAKE, FAKE, None, FAKE, 100, 64, 64, FAKE, need - 1, None) == WORKSPACE
+    assert h(FAKE, FAKE, FAKE, None, FAKE, 100, 64, 64, None, need, None) == WORKSPACE
+    assert h(FAKE, FAKE, FAKE, None, FAKE, 100, 64, 64, FAKE + 4, need, None) == ALIGN
+    k = lib.bsfp4_int8_gated_ffn
+    assert k(FAKE, FAKE, FAKE, FAKE, 3, FAKE, 2, 64, 64, None, 0, None) == INVALID and "activation" in err(lib)
+    assert k(FAKE, FAKE, FAKE, FAKE, 0, FAKE, 2, 60, 64, None, 0, None) == SHAPE
+
+
+def test_abi_gated(lib):
+    f = lib.bsfp4_gated_ffn
+    assert f(FAKE, FAKE, -1, FAKE, None, 2, 64, 64, None, 0, None) == INVALID
+    assert f(FAKE, FAKE, 0, FAKE, None, 2, 64, 60, None, 0, None) == SHAPE
+    assert f(FAKE, FAKE, 0, FAKE, None, 2, 64, 1 << 22, None, 0, None) == SHAPE and "2^22" in err(lib)
+    assert f(FAKE, FAKE, 0, FAKE, None, 2, 1 << 21, 64, None, 0, None) == SHAPE
+    assert f(FAKE, None, 0, FAKE, None, 2, 64, 64, None, 0, None) == INVALID
+    assert f(FAKE, FAKE, 0, FAKE, FAKE + 2, 2, 64, 64, None, 0, None) == ALIGN
+    b = lib.bsfp4_gated_ffn_backward
+    need = lib.bsfp4_gated_ffn_backward_workspace_size(100, 64, 64)
+    assert need >= 100 * 128 * 2
+    assert b(FAKE, FAKE, FAKE, FAKE, 0, FAKE, FAKE, 100, 64, 64, FAKE, need - 1, None) == WORKSPACE
+    assert b(FAKE, FAKE, FAKE, FAKE, 0, None, None, 100, 64, 64, FAKE, need, None) == INVALID
+    assert b(FAKE, FAKE, FAKE, FAKE, 0, FAKE + 8, FAKE, 100, 64, 64, FAKE, need, None) == ALIGN
+    assert b(FAKE, None, FAKE, FAKE, 0, FAKE, FAKE, 100, 64, 64, FAKE, need, None) == INVALID
+    assert b(None, None, FAKE, None, 0, FAKE, None, 0, 64, 64, FAKE, need, None) == OK
+
+
+def test_abi_block_norm(lib):
+    def call(back=False, ws=FAKE, n=1 << 30, **kw):
+        a = binding.BlockNormArgs(scale=1.0, eps=1e-6, T=4, H=64, groups=1, residual=FAKE)
+        for k, v in kw.items():
+            setattr(a, k, v)
+        if back:
+            return lib.bsfp4_block_norm_backward(ctypes.byref(a), ws, n, None)
+        return lib.bsfp4_block_norm(ctypes.byref(a), None)
+
+    assert lib.bsfp4_block_norm(None, None) == INVALID
+    assert call(H=60) == SHAPE and call(H=16392) == SHAPE and call(T=-1) == SHAPE and call(groups=0) == SHAPE
+    assert call(x=FAKE, res_out=FAKE, gate=FAKE, groups=3) == SHAPE
+    assert call(x=FAKE, res_out=FAKE, groups=2) == SHAPE and "without a gate" in err(lib)
+    assert call(x=FAKE, res_out=FAKE, eps=0.0) == INVALID
+    assert call() == INVALID                                    # neither x nor w_pre
+    assert call(w_post=FAKE, w_pre=FAKE, z=FAKE) == INVALID     # w_post without x
+    assert call(x=FAKE) == INVALID                              # no res_out
+    assert call(w_pre=FAKE) == INVALID                          # no z
+    assert call(w_pre=FAKE, z=FAKE, q=FAKE, s=FAKE) == INVALID
+    assert call(w_pre=FAKE, q=FAKE) == INVALID
+    assert call(x=FAKE, res_out=FAKE, z=FAKE) == INVALID        # z without w_pre
+    assert call(w_pre=FAKE + 8, z=FAKE) == ALIGN and "w_pre" in err(lib)
+    assert call(w_pre=FAKE, z=FAKE, residual=None) == INVALID
+    assert call(T=0, residual=None, w_pre=FAKE) == OK
+    b = dict(back=True, x=FAKE, w_post=FAKE, w_pre=FAKE, res_out=FAKE, dz=FAKE, dx=FAKE, dres=FAKE, dw_post=FAKE,
+             dw_pre=FAKE)
+    for missing in ("res_out", "dz", "dx", "dres", "dw_post", "dw_pre"):
+        assert call(**{**b, missing: None}) == INVALID, missing
+    assert call(**b, gate=FAKE) == INVALID and "dgate" in err(lib)
+    assert call(**b, n=16) == WORKSPACE
