@@ -180,7 +180,13 @@ def _p(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# the current stream's handle without the Python Stream object around it, where this torch has it (1.8 us less a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device) -> ctypes.c_void_p:
+    if _raw_stream is not None and device.index is not None:
+        return ctypes.c_void_p(_raw_stream(device.index))
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
@@ -210,17 +216,17 @@ def _numel(t, n, name):
 
 def _device(*named):
     """Every given tensor must be a GPU tensor, all on the same device."""
-    dev = None
+    first, index = None, -1
     for t, name in named:
         if t is None:
             continue
-        if t.device.type != "cuda":
+        if not t.is_cuda:
             raise ValueError(f"{name} must be a device tensor (got {t.device})")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    return dev
+        if first is None:
+            first, index = t, t.get_device()
+        elif t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+    return None if first is None else first.device
 
 
 def _workspace(nbytes: int, device):
@@ -421,11 +427,35 @@ def _multiple(v, step, name):
         raise ValueError(f"{name}={v} is not a multiple of {step}")
 
 
-def _call(dev, what, fn, args, ws_bytes):
-    """fn(*args, ws, ws_bytes, stream) on the tensors' device and its current stream."""
+def _a(t):
+    """A tensor's address as ctypes takes it fastest."""
+    return None if t is None else t.data_ptr()
+
+
+def _launch(dev, what, fn, *args):
+    """fn(*args, stream) with the tensors' device as the current one, on its current stream."""
+    if torch.cuda.current_device() == dev.index:
+        status = fn(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _stream(dev))
+    if status != 0:
+        _check(status, what)
+
+
+def _ws_bytes(dev, fn, *sizes) -> int:
+    """A workspace size; the plan behind it goes by the tensors' device."""
+    if torch.cuda.current_device() == dev.index:
+        return fn(*sizes)
     with torch.cuda.device(dev):
-        ws = _workspace(ws_bytes, dev)
-        _check(fn(*args, _p(ws), ws_bytes, _stream(dev)), what)
+        return fn(*sizes)
+
+
+def _call(dev, what, fn, args, size_fn, sizes):
+    """_launch with the workspace that the call needs."""
+    n = _ws_bytes(dev, size_fn, *sizes)
+    ws = _workspace(n, dev)
+    _launch(dev, what, fn, *args, _a(ws), n)
 
 
 def int8_quantize(x: torch.Tensor, q: torch.Tensor | None = None, s: torch.Tensor | None = None):
@@ -442,8 +472,7 @@ def int8_quantize(x: torch.Tensor, q: torch.Tensor | None = None, s: torch.Tenso
         q = torch.empty((M, K), dtype=torch.int8, device=dev)
     if s is None:
         s = torch.empty(M, dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
-        _check(load().bsfp4_int8_quantize(_p(x), M, K, _p(q), _p(s), _stream(dev)), "bsfp4_int8_quantize")
+    _launch(dev, "bsfp4_int8_quantize", load().bsfp4_int8_quantize, _a(x), M, K, _a(q), _a(s))
     return q, s
 
 
@@ -479,7 +508,7 @@ def int8_gemm(A, SA, B, SB, bias: torch.Tensor | None = None, out: torch.Tensor 
     D = out if out is not None else torch.empty((M, N), dtype=torch.bfloat16, device=dev)
     lib = load()
     _call(dev, "bsfp4_int8_gemm", lib.bsfp4_int8_gemm,
-          (_p(A), _p(SA), _p(B), _p(SB), _p(bias), _p(D), M, N, K), lib.bsfp4_int8_gemm_workspace_size(M, N, K))
+          (_a(A), _a(SA), _a(B), _a(SB), _a(bias), _a(D), M, N, K), lib.bsfp4_int8_gemm_workspace_size, (M, N, K))
     return D
 
 
@@ -497,7 +526,7 @@ def int8_quantize_gemm(x, B, SB, bias: torch.Tensor | None = None, out: torch.Te
     D = out if out is not None else torch.empty((M, N), dtype=torch.bfloat16, device=dev)
     lib = load()
     _call(dev, "bsfp4_int8_quantize_gemm", lib.bsfp4_int8_quantize_gemm,
-          (_p(x), _p(B), _p(SB), _p(bias), _p(D), M, N, K), lib.bsfp4_int8_quantize_gemm_workspace_size(M, N, K))
+          (_a(x), _a(B), _a(SB), _a(bias), _a(D), M, N, K), lib.bsfp4_int8_quantize_gemm_workspace_size, (M, N, K))
     return D
 
 
@@ -525,7 +554,7 @@ def int8_gated_ffn(A, SA, W13, SW13, act="silu", out: torch.Tensor | None = None
     h = out if out is not None else torch.empty((M, I), dtype=torch.bfloat16, device=dev)
     lib = load()
     _call(dev, "bsfp4_int8_gated_ffn", lib.bsfp4_int8_gated_ffn,
-          (_p(A), _p(SA), _p(W13), _p(SW13), a, _p(h), M, I, K), lib.bsfp4_int8_gated_ffn_workspace_size(M, I, K))
+          (_a(A), _a(SA), _a(W13), _a(SW13), a, _a(h), M, I, K), lib.bsfp4_int8_gated_ffn_workspace_size, (M, I, K))
     return h
 
 
@@ -543,27 +572,27 @@ def _gated_args(x, W13):
 
 def gated_ffn(x, W13, act="silu", save_gate_up: bool = False, out: torch.Tensor | None = None):
     """h = bf16(act(G) * U), [G | U] = x @ W13^T; x bf16 [M, H], W13 bf16 [2 I, H] (gate rows, then up rows).
-    With save_gate_up returns (h, bf16 [G | U]) for gated_ffn_backward."""
+    With save_gate_up returns (h, float32 [G | U]) for gated_ffn_backward."""
     a = _act(act)
     M, H, I = _gated_args(x, W13)
     _out(out, (M, I), torch.bfloat16, "out")
     dev = _device((x, "x"), (W13, "W13"), (out, "out"))
     h = out if out is not None else torch.empty((M, I), dtype=torch.bfloat16, device=dev)
-    gate_up = torch.empty((M, 2 * I), dtype=torch.bfloat16, device=dev) if save_gate_up else None
+    gate_up = torch.empty((M, 2 * I), dtype=torch.float32, device=dev) if save_gate_up else None
     lib = load()
-    _call(dev, "bsfp4_gated_ffn", lib.bsfp4_gated_ffn, (_p(x), _p(W13), a, _p(h), _p(gate_up), M, I, H),
-          lib.bsfp4_gated_ffn_workspace_size(M, I, H))
+    _call(dev, "bsfp4_gated_ffn", lib.bsfp4_gated_ffn, (_a(x), _a(W13), a, _a(h), _a(gate_up), M, I, H),
+          lib.bsfp4_gated_ffn_workspace_size, (M, I, H))
     return (h, gate_up) if save_gate_up else h
 
 
 def gated_ffn_backward(dh, x, W13, gate_up, act="silu", need_dx: bool = True, need_dW13: bool = True):
-    """Gradients (dx [M, H], dW13 [2 I, H]) of gated_ffn from dh [M, I] and the saved gate_up [M, 2 I], all
-    bf16; None for one that is not needed."""
+    """Gradients (dx [M, H], dW13 [2 I, H]) of gated_ffn from dh [M, I] and the saved gate_up
+    (float32 [M, 2 I]), the rest bf16; None for one that is not needed."""
     a = _act(act)
     M, H, I = _gated_args(x, W13)
     _need(dh, torch.bfloat16, "dh")
     _shape(dh, (M, I), "dh")
-    _need(gate_up, torch.bfloat16, "gate_up")
+    _need(gate_up, torch.float32, "gate_up")
     _shape(gate_up, (M, 2 * I), "gate_up")
     dev = _device((dh, "dh"), (x, "x"), (W13, "W13"), (gate_up, "gate_up"))
     dx = torch.empty((M, H), dtype=torch.bfloat16, device=dev) if need_dx else None
@@ -572,8 +601,8 @@ def gated_ffn_backward(dh, x, W13, gate_up, act="silu", need_dx: bool = True, ne
         return None, None
     lib = load()
     _call(dev, "bsfp4_gated_ffn_backward", lib.bsfp4_gated_ffn_backward,
-          (_p(dh), _p(x), _p(W13), _p(gate_up), a, _p(dx), _p(dW), M, I, H),
-          lib.bsfp4_gated_ffn_backward_workspace_size(M, I, H))
+          (_a(dh), _a(x), _a(W13), _a(gate_up), a, _a(dx), _a(dW), M, I, H),
+          lib.bsfp4_gated_ffn_backward_workspace_size, (M, I, H))
     return dx, dW
 
 
@@ -647,8 +676,7 @@ def block_norm(x, residual, w_post=None, w_pre=None, gate=None, scale: float = 1
         outs = (torch.empty((T, H), dtype=torch.int8, device=dev), torch.empty(T, dtype=torch.float32, device=dev))
         _fill(a, q=outs[0], s=outs[1])
     _fill(a, x=x, residual=residual, w_post=w_post, w_pre=w_pre, gate=gate)
-    with torch.cuda.device(dev):
-        _check(load().bsfp4_block_norm(ctypes.byref(a), _stream(dev)), "bsfp4_block_norm")
+    _launch(dev, "bsfp4_block_norm", load().bsfp4_block_norm, ctypes.byref(a))
     return (res, *outs) if outs else res
 
 
@@ -678,7 +706,7 @@ def block_norm_backward(dres, dz, x, res, w_post=None, w_pre=None, gate=None, sc
           dw_post=dw_post, dw_pre=dw_pre, dgate=dgate)
     lib = load()
     _call(dev, "bsfp4_block_norm_backward", lib.bsfp4_block_norm_backward, (ctypes.byref(a),),
-          lib.bsfp4_block_norm_backward_workspace_size(T, H, a.groups))
+          lib.bsfp4_block_norm_backward_workspace_size, (T, H, a.groups))
     return dx, dresidual, dw_post, dw_pre, dgate
 
 

@@ -378,7 +378,7 @@ bsfp4_status bsfp4_int8_gemm(const int8_t* A, const float* sa, const int8_t* B, 
 }
 
 size_t bsfp4_int8_quantize_gemm_workspace_size(int64_t M, int64_t N, int64_t K) {
-  if (M <= 0 || N <= 0 || K <= 0) return 0;
+  if (M <= 0 || N <= 0 || K <= 0 || bsfp4::int8_fused_quant_ok(M, K)) return 0;
   return round256((size_t)M * K) + round256((size_t)M * sizeof(float)) + bsfp4::int8_gemm_workspace(M, N, K);
 }
 
@@ -397,6 +397,9 @@ bsfp4_status bsfp4_int8_quantize_gemm(const uint16_t* x, const int8_t* B, const 
   if (bsfp4_status e = check_workspace(ws, ws_bytes, bsfp4_int8_quantize_gemm_workspace_size(M, N, K))) return e;
   if (M == 0) return ok();
   if (bsfp4_status e = check_device()) return e;
+  if (bsfp4::int8_fused_quant_ok(M, K))
+    return launched(bsfp4::launch_int8_fused_quant_gemm(x, B, sb, bias, D, M, N, K, as_stream(stream)),
+                    "bsfp4_int8_quantize_gemm launch");
   int8_t* q = static_cast<int8_t*>(ws);
   float* s = reinterpret_cast<float*>(q + round256((size_t)M * K));
   void* rest = reinterpret_cast<uint8_t*>(s) + round256((size_t)M * sizeof(float));
@@ -446,7 +449,7 @@ size_t bsfp4_gated_ffn_workspace_size(int64_t M, int64_t I, int64_t H) {
   return bsfp4::gated_ffn_workspace(M, I, H);
 }
 
-bsfp4_status bsfp4_gated_ffn(const uint16_t* x, const uint16_t* W, int act, uint16_t* h, uint16_t* gate_up, int64_t M,
+bsfp4_status bsfp4_gated_ffn(const uint16_t* x, const uint16_t* W, int act, uint16_t* h, float* gate_up, int64_t M,
                              int64_t I, int64_t H, void* ws, size_t ws_bytes, void* stream) {
   if (bsfp4_status e = check_gated(act, M, I, H)) return e;
   if (M > 0) {
@@ -468,7 +471,7 @@ size_t bsfp4_gated_ffn_backward_workspace_size(int64_t M, int64_t I, int64_t H) 
 }
 
 bsfp4_status bsfp4_gated_ffn_backward(const uint16_t* dh, const uint16_t* x, const uint16_t* W,
-                                      const uint16_t* gate_up, int act, uint16_t* dx, uint16_t* dW, int64_t M,
+                                      const float* gate_up, int act, uint16_t* dx, uint16_t* dW, int64_t M,
                                       int64_t I, int64_t H, void* ws, size_t ws_bytes, void* stream) {
   if (bsfp4_status e = check_gated(act, M, I, H)) return e;
   if (M > 0) {

@@ -6,12 +6,37 @@
 // |acc| <= 2^14 K below 2^31.  Its conversion to binary32 and the two scale
 // products round once each; split K adds integers, so D does not depend on the
 // split.
-#include "tile_gemm.h"
+#include "rows_gemm.h"
 
 namespace bsfp4 {
+namespace {
+
+// Rows up to which every workgroup of the product quantises the activations for
+// itself: each reads all of x, so the work grows with M while the launch saved
+// does not.
+constexpr int64_t kFusedQuantRows = 4;
+
+}  // namespace
 
 size_t int8_gemm_workspace(int64_t M, int64_t N, int64_t K) {
+  if (rows_ok(M)) return 0;
   return tile_workspace(plan_tile(M, N, K, device_cu_count()), M, N);
+}
+
+bool int8_fused_quant_ok(int64_t M, int64_t K) { return M <= kFusedQuantRows && M * K <= kRowsQuantBytes; }
+
+hipError_t launch_int8_fused_quant_gemm(const uint16_t* x, const int8_t* B, const float* sb, const uint16_t* bias,
+                                        uint16_t* D, int64_t M, int64_t N, int64_t K, hipStream_t stream) {
+  TileArgs a{};
+  a.B = reinterpret_cast<const uint8_t*>(B);
+  a.ldb = K;
+  a.M = (int)M;
+  a.N = (int)N;
+  a.kend = K;
+  a.sb = sb;
+  a.bias = bias;
+  a.D = D;
+  return launch_rows_shape<true, kTileStore, 1, 1, true>(a, x, stream);
 }
 
 size_t int8_gated_workspace(int64_t M, int64_t I, int64_t K) { return int8_gemm_workspace(M, 2 * I, K); }
@@ -30,6 +55,7 @@ hipError_t launch_int8_gemm(const int8_t* A, const float* sa, const int8_t* B, c
   a.bias = bias;
   a.D = D;
   a.part = ws;
+  if (rows_ok(M)) return launch_rows<true, kTileStore>(a, stream);
   return launch_tile<true, false, false, kTileStore>(a, plan_tile(M, N, K, device_cu_count()), stream);
 }
 
@@ -47,6 +73,7 @@ hipError_t launch_int8_gated(const int8_t* A, const float* sa, const int8_t* W, 
   a.act = act;
   a.D = D;
   a.part = ws;
+  if (rows_ok(M)) return launch_rows<true, kTileGated>(a, stream);
   return launch_tile<true, false, false, kTileGated>(a, plan_tile(M, 2 * I, K, device_cu_count()), stream);
 }
 

@@ -119,6 +119,10 @@ hipError_t launch_int8_quant(const uint16_t* x, int64_t M, int64_t K, int8_t* q,
 
 // 8-bit products (gemm_int8.hip; K % 16 == 0, N % 8 == 0); gated: W [2 I, K].
 size_t int8_gemm_workspace(int64_t M, int64_t N, int64_t K);
+// x quantised inside the product's workgroups (few rows): no intermediate, one launch.
+bool int8_fused_quant_ok(int64_t M, int64_t K);
+hipError_t launch_int8_fused_quant_gemm(const uint16_t* x, const int8_t* B, const float* sb, const uint16_t* bias,
+                                        uint16_t* D, int64_t M, int64_t N, int64_t K, hipStream_t stream);
 size_t int8_gated_workspace(int64_t M, int64_t I, int64_t K);
 hipError_t launch_int8_gemm(const int8_t* A, const float* sa, const int8_t* B, const float* sb, const uint16_t* bias,
                             uint16_t* D, int64_t M, int64_t N, int64_t K, void* ws, hipStream_t stream);
@@ -128,10 +132,10 @@ hipError_t launch_int8_gated(const int8_t* A, const float* sa, const int8_t* W, 
 // Gated feed-forward product in bf16 (gated_ffn.hip; H % 8 == 0, I % 8 == 0).
 constexpr int kActSilu = 0, kActGelu = 1, kActGeluTanh = 2;
 size_t gated_ffn_workspace(int64_t M, int64_t I, int64_t H);
-hipError_t launch_gated_ffn(const uint16_t* x, const uint16_t* W, int act, uint16_t* h, uint16_t* gate_up, int64_t M,
+hipError_t launch_gated_ffn(const uint16_t* x, const uint16_t* W, int act, uint16_t* h, float* gate_up, int64_t M,
                             int64_t I, int64_t H, void* ws, hipStream_t stream);
 size_t gated_ffn_bwd_workspace(int64_t M, int64_t I, int64_t H);
-hipError_t launch_gated_ffn_bwd(const uint16_t* dh, const uint16_t* x, const uint16_t* W, const uint16_t* gate_up,
+hipError_t launch_gated_ffn_bwd(const uint16_t* dh, const uint16_t* x, const uint16_t* W, const float* gate_up,
                                 int act, uint16_t* dx, uint16_t* dW, int64_t M, int64_t I, int64_t H, void* ws,
                                 hipStream_t stream);
 

@@ -163,24 +163,24 @@ struct TileLoader {
     }
   }
 
-  // Stage `st` (of kb bytes of K, or k rows) into LDS at `lds`.
-  __device__ __forceinline__ void issue(int st, int64_t kend, uint32_t lds) const {
-    if constexpr (kTrans) {
-      const int64_t k = (int64_t)st * kTileStageK;
-      const int left = (int)min((int64_t)kTileStageK, kend - k);
-      const v4u32 r = make_rsrc4(base + k * ld, (int64_t)left * ld - cols);
+  // Before the loads of the last stage, `left` bytes of K wide: chunks past K read as zeros.
+  __device__ __forceinline__ void mask_tail(int left) {
+    if constexpr (!kTrans) {
 #pragma unroll
-      for (int j = 0; j < kLoads; j++) buf_lds16(r, off[j], 0, lds + (uint32_t)(q0 + j) * 1024);
-    } else {
-      const uint32_t soff = (uint32_t)st * kTileStage;
-      const int left = (int)min((int64_t)kTileStage, kend - (int64_t)soff);
-#pragma unroll
-      for (int j = 0; j < kLoads; j++) {
-        const v4u32 r = kPairs && (((q0 + j) >> 2) & 1) ? rsrc[kPairs ? 1 : 0] : rsrc[0];
-        const uint32_t v = (int)c16[j] < left ? off[j] : kBufOOB;
-        buf_lds16(r, v, soff, lds + (uint32_t)(q0 + j) * 1024);
-      }
+      for (int j = 0; j < kLoads; j++) off[j] = (int)c16[j] < left ? off[j] : kBufOOB;
     }
+  }
+
+  // The buffer of a stage (transposed: `k0` its first k row, `left` rows of it)
+  __device__ __forceinline__ v4u32 stage_rsrc(int64_t k0, int64_t left) const {
+    if constexpr (kTrans) return make_rsrc4(base + k0 * ld, min(left, (int64_t)kTileStageK) * ld - cols);
+    else return rsrc[0];
+  }
+
+  // Load j of stage `st` into LDS at `lds`.
+  __device__ __forceinline__ void issue(int j, int st, v4u32 r, uint32_t lds) const {
+    if (kPairs && (((q0 + j) >> 2) & 1)) r = rsrc[kPairs ? 1 : 0];
+    buf_lds16(r, off[j], kTrans ? 0u : (uint32_t)st * kTileStage, lds + (uint32_t)(q0 + j) * 1024);
   }
 };
 
@@ -233,7 +233,7 @@ struct TileArgs {
   const float* sb;     // 8-bit: scale per row of B
   const uint16_t* bias;  // [N] or null (store)
   uint16_t* D;         // [M, N]
-  uint16_t* gate_up;   // gated: bf16 [M, 2 N] or null
+  float* gate_up;      // gated: the sums [M, 2 N] or null
   int act;
   int tiles_m, tiles_n, splits;
   void* part;          // splits > 1: float / int32 [splits][M][N or 2 N]
@@ -309,47 +309,92 @@ __global__ void __launch_bounds__(64 * WGM * WGN, (tile_waves_simd<BM, BN, WGM *
   ra.init(wm * TM, lane);
   rb.init(wn * TN, lane);
   const uint32_t lds0 = lds_offset(smem);
-  auto issue = [&](int st) {
-    const uint32_t slot = lds0 + (uint32_t)(st & 1) * kStage;
-    la.issue(st, kend_a, slot);
-    lb.issue(st, kend_b, slot + kStageA);
-  };
-
   typename MM::Acc acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; i++)
 #pragma unroll
     for (int j = 0; j < TN; j++) acc[i][j] = typename MM::Acc{};
 
-  if (s0 < s1) issue(s0);
-  for (int st = s0; st < s1; st++) {
-    wait_vmcnt<0>();  // this wave's loads of stage st
-    __builtin_amdgcn_s_barrier();  // everyone's; and everyone is done with the other slot
+  // A stage is four groups kk of TM x TN MFMAs.  The fragments of the next group
+  // are read, and the loads of the stage after next issued, between a group's
+  // MFMAs.  The one barrier of a stage stands in the middle of group 2, where the
+  // wave has all fragments of the stage in registers: past it every wave's loads
+  // of the next stage have landed and the slot just read is free, so group 3
+  // already reads the next stage and the MFMAs run on across it.
+  constexpr int kMfma = TM * TN, kReads = TM + TN;
+  constexpr int kIssues = decltype(la)::kLoads + decltype(lb)::kLoads;
+  v4i fa[2][TM], fb[2][TN];
+  auto read_one = [&](int r, int slot, int kk, int buf) {  // fragment r of group kk: B's, then A's
+    const uint8_t* q = smem + slot * kStage;
+    if (r < TN) fb[buf][r] = rb.read(q + kStageA, r, kk);
+    else fa[buf][r - TN] = ra.read(q, r - TN, kk);
+  };
+  v4u32 rsa, rsb;
+  auto begin_issue = [&](int st) {  // before the loads of stage st
+    if (st + 1 == total) {
+      la.mask_tail((int)(kend_a - (int64_t)st * kTileStage));
+      lb.mask_tail((int)(kend_b - (int64_t)st * kTileStage));
+    }
+    rsa = la.stage_rsrc((int64_t)st * kTileStageK, kend_a - (int64_t)st * kTileStageK);
+    rsb = lb.stage_rsrc((int64_t)st * kTileStageK, kend_b - (int64_t)st * kTileStageK);
+  };
+  auto issue_one = [&](int j, int st) {
+    const uint32_t slot = lds0 + (uint32_t)(st & 1) * kStage;
+    if (j < decltype(la)::kLoads) la.issue(j, st, rsa, slot);
+    else lb.issue(j - decltype(la)::kLoads, st, rsb, slot + kStageA);
+  };
+  auto arrive = [&] {
+    // this wave's loads of the next stage and its last reads of this one
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if (st + 1 < s1) issue(st + 1);
-    const uint8_t* qa = smem + (st & 1) * kStage;
-    const uint8_t* qb = qa + kStageA;
-    v4i fa[2][TM], fb[2][TN];
+  };
+  // kNext: a stage follows;  kAfter: two do
+  auto group = [&](auto next_c, auto after_c, int kk, int st) {
+    constexpr bool kNext = decltype(next_c)::value, kAfter = decltype(after_c)::value;
+    if (kAfter && kk == 3) begin_issue(st + 2);
 #pragma unroll
-    for (int j = 0; j < TN; j++) fb[0][j] = rb.read(qb, j, 0);
-#pragma unroll
-    for (int i = 0; i < TM; i++) fa[0][i] = ra.read(qa, i, 0);
-#pragma unroll
-    for (int kk = 0; kk < 4; kk++) {
-      if (kk < 3) {
-#pragma unroll
-        for (int j = 0; j < TN; j++) fb[(kk + 1) & 1][j] = rb.read(qb, j, kk + 1);
-#pragma unroll
-        for (int i = 0; i < TM; i++) fa[(kk + 1) & 1][i] = ra.read(qa, i, kk + 1);
-      }
+    for (int t = 0; t < kMfma; t++) {
+      const int i = t / TN, j = t % TN;
       // the B fragment as first operand: a lane ends with four consecutive
       // columns of one row in each register quad
+      acc[i][j] = MM::run(fb[kk & 1][j], fa[kk & 1][i], acc[i][j]);
+      if (kk < 3 || kNext) {
 #pragma unroll
-      for (int i = 0; i < TM; i++)
+        for (int r = 0; r < kReads; r++)
+          if (r * (kMfma / 4) / kReads == t) read_one(r, (st + (kk == 3)) & 1, (kk + 1) & 3, (kk + 1) & 1);
+      }
+      if (kNext && kk == 2 && t == kMfma * 3 / 4 - 1) arrive();
+      if (kAfter && kk == 3) {
 #pragma unroll
-        for (int j = 0; j < TN; j++) acc[i][j] = MM::run(fb[kk & 1][j], fa[kk & 1][i], acc[i][j]);
+        for (int l = 0; l < kIssues; l++)
+          if (l * kMfma / kIssues == t) issue_one(l, st + 2);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
-    asm volatile("" ::: "memory");
+  };
+  auto stage = [&](auto next_c, auto after_c, int st) {
+    group(next_c, after_c, 0, st);
+    group(next_c, after_c, 1, st);
+    group(next_c, after_c, 2, st);
+    group(next_c, after_c, 3, st);
+  };
+  if (s0 < s1) {
+    begin_issue(s0);
+#pragma unroll
+    for (int l = 0; l < kIssues; l++) issue_one(l, s0);
+    arrive();
+    if (s0 + 1 < s1) {
+      begin_issue(s0 + 1);
+#pragma unroll
+      for (int l = 0; l < kIssues; l++) issue_one(l, s0 + 1);
+    }
+#pragma unroll
+    for (int r = 0; r < kReads; r++) read_one(r, s0 & 1, 0, 0);
+    int st = s0;
+    for (; st + 2 < s1; st++) stage(std::true_type{}, std::true_type{}, st);
+    if (st + 1 < s1) stage(std::true_type{}, std::false_type{}, st++);
+    stage(std::false_type{}, std::false_type{}, st);
   }
 
   // register 4q + e of block (i, j): row wm*WM + 32 i + lr, tile column wn*WN + 32 j + 8q + 4g + e
@@ -430,31 +475,49 @@ __global__ void __launch_bounds__(64 * WGM * WGN, (tile_waves_simd<BM, BN, WGM *
       }
     flush(p.D, p.N);
   } else {
-    // pass 0: h = act(gate) * up; with gate_up, pass 1: gate, pass 2: up
-    const int passes = p.gate_up ? 3 : 1;
-    for (int pass = 0; pass < passes; pass++) {
-      if (pass > 0) __syncthreads();
 #pragma unroll
-      for (int j = 0; j < TN; j += 2)
+    for (int j = 0; j < TN; j += 2)
 #pragma unroll
-        for (int q = 0; q < 4; q++) {
-          const int c = wn * (WN / 2) + (j / 2) * 32 + 8 * q + 4 * g, n = min(n0 + c, p.N - 4);
-          const float4 sg = scales(n), su = scales(p.N + n);
+      for (int q = 0; q < 4; q++) {
+        const int c = wn * (WN / 2) + (j / 2) * 32 + 8 * q + 4 * g, n = min(n0 + c, p.N - 4);
+        const float4 sg = scales(n), su = scales(p.N + n);
 #pragma unroll
-          for (int i = 0; i < TM; i++) {
-            const float4 gv = quad(i, j, q, sg), uv = quad(i, j + 1, q, su);
-            float4 v;
-            if (pass == 0)
-              v = make_float4(act_value(p.act, gv.x) * uv.x, act_value(p.act, gv.y) * uv.y,
-                              act_value(p.act, gv.z) * uv.z, act_value(p.act, gv.w) * uv.w);
-            else
-              v = pass == 1 ? gv : uv;
-            *reinterpret_cast<uint2*>(smem + (wm * WM + i * 32 + lr) * kPitch + c * 2) =
-                make_uint2(pack_bf16x2_ieee(v.x, v.y), pack_bf16x2_ieee(v.z, v.w));
+        for (int i = 0; i < TM; i++) {
+          const float4 gv = quad(i, j, q, sg), uv = quad(i, j + 1, q, su);
+          const int r = wm * WM + i * 32 + lr;
+          *reinterpret_cast<uint2*>(smem + r * kPitch + c * 2) =
+              make_uint2(pack_bf16x2_ieee(act_value(p.act, gv.x) * uv.x, act_value(p.act, gv.y) * uv.y),
+                         pack_bf16x2_ieee(act_value(p.act, gv.z) * uv.z, act_value(p.act, gv.w) * uv.w));
+        }
+      }
+    flush(p.D, p.N);
+    if constexpr (!kInt8) {
+      if (p.gate_up) {  // the sums as they are, gate then up, in whole row segments as well
+        constexpr int kPitch4 = kCols * 4 + 16;
+        static_assert(BM * kPitch4 <= tile_smem<BM, BN>(), "a binary32 half tile fits in LDS");
+#pragma unroll
+        for (int half = 0; half < 2; half++) {
+          __syncthreads();
+#pragma unroll
+          for (int j = half; j < TN; j += 2)
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+              const int c = wn * (WN / 2) + (j / 2) * 32 + 8 * q + 4 * g;
+#pragma unroll
+              for (int i = 0; i < TM; i++)
+                *reinterpret_cast<float4*>(smem + (wm * WM + i * 32 + lr) * kPitch4 + c * 4) =
+                    make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+            }
+          __syncthreads();
+          constexpr int kChunksRow = kCols / 4;
+          for (int idx = tid; idx < BM * kChunksRow; idx += NT) {
+            const int r = idx / kChunksRow, c = (idx % kChunksRow) * 4;
+            if (m0 + r < p.M && n0 + c < p.N)
+              *reinterpret_cast<float4*>(p.gate_up + (int64_t)(m0 + r) * 2 * p.N + half * p.N + n0 + c) =
+                  *reinterpret_cast<const float4*>(smem + r * kPitch4 + c * 4);
           }
         }
-      if (pass == 0) flush(p.D, p.N);
-      else flush(p.gate_up + (pass == 1 ? 0 : p.N), 2 * (int64_t)p.N);
+      }
     }
   }
 }
@@ -493,8 +556,12 @@ __global__ void __launch_bounds__(256)
       float u[8];
       sum8(p.N + n, p.sb, u);
       if (p.gate_up) {
-        *reinterpret_cast<uint4*>(p.gate_up + m * width + n) = pack8(v);
-        *reinterpret_cast<uint4*>(p.gate_up + m * width + p.N + n) = pack8(u);
+        float4* dg = reinterpret_cast<float4*>(p.gate_up + m * width + n);
+        float4* du = reinterpret_cast<float4*>(p.gate_up + m * width + p.N + n);
+        dg[0] = make_float4(v[0], v[1], v[2], v[3]);
+        dg[1] = make_float4(v[4], v[5], v[6], v[7]);
+        du[0] = make_float4(u[0], u[1], u[2], u[3]);
+        du[1] = make_float4(u[4], u[5], u[6], u[7]);
       }
 #pragma unroll
       for (int k = 0; k < 8; k++) v[k] = act_value(p.act, v[k]) * u[k];
@@ -513,31 +580,38 @@ struct TilePlan {
   int bm, bn, splits;
 };
 
-// Tile shape and K split of an M x N (x K bytes) product: the shape whose
-// estimated time is least.  Time = rounds of workgroups x (bytes of K per split /
-// measured bytes of K a workgroup takes per second) + a fixed part per round +
-// the partials' traffic and the second launch of a split.  N counts weight rows
-// (gated: both halves).
+// Tile shape and K split of an M x N (x K bytes) product: the pair with the least
+// estimated time.  A compute unit holds one 256 x 256 workgroup, two of 128 x 128
+// or three of 64 x 128; a stage takes a workgroup us[c - 1] microseconds when c
+// share the unit, a workgroup's start and end cost kRoundUs, a split's second
+// kernel kSplitUs and its partials their bytes.  The figures are a least-squares
+// fit to 460 timed (shape, tile, split) combinations, M 32 .. 1024, weights of 1536 x
+// 2048 .. 14336 x 4096, bf16 and int8 (10 % rms); the plan's choice is 3 % slower
+// than the best of each shape on average.  N counts weight rows (gated: both
+// halves).
 inline TilePlan plan_tile(int64_t M, int64_t N, int64_t kbytes, int cus) {
   struct Cand {
     int bm, bn, per_cu;
-    double us_stage;  // microseconds a stage of 128 bytes takes a workgroup, the CU full
+    double us[3];
   };
-  static constexpr Cand cands[] = {{256, 256, 1, 1.0}, {128, 128, 2, 0.55}, {64, 128, 3, 0.45}};
+  static constexpr Cand cands[] = {{256, 256, 1, {1.06, 0, 0}}, {128, 128, 2, {0.60, 0.80, 0}}, {64, 128, 3, {0.52, 0.64, 0.73}}};
+  static constexpr double kRoundUs[] = {3.9, 2.2, 2.1}, kSplitUs = 2.8, kPartBytesUs = 4.5e6;
   const int64_t stages = (kbytes + kTileStage - 1) / kTileStage;
   TilePlan best{256, 256, 1};
   double best_t = 1e300;
-  for (const Cand& c : cands) {
-    const int64_t tiles = ((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
+  for (int c = 0; c < 3; c++) {
+    const Cand& cd = cands[c];
+    const int64_t tiles = ((M + cd.bm - 1) / cd.bm) * ((N + cd.bn - 1) / cd.bn);
+    const int64_t slots = (int64_t)cus * cd.per_cu;
     for (int sp = 1; sp <= 16; sp++) {
-      if (sp > 1 && stages / sp < 4) break;
-      const int64_t slots = (int64_t)cus * c.per_cu;
-      const int64_t rounds = (tiles * sp + slots - 1) / slots;
-      double t = rounds * ((double)((stages + sp - 1) / sp) * c.us_stage + 2.0);
-      if (sp > 1) t += 2.0 * sp * M * N * 4 / 5.0e6 + 3.0;
+      if (sp > 1 && (stages / sp < 4 || tiles * (sp - 1) >= slots)) break;
+      const int64_t items = tiles * sp, full = items / slots, rest = (items % slots + cus - 1) / cus;
+      const double per = (double)((stages + sp - 1) / sp);
+      double t = kRoundUs[c] + full * per * cd.us[cd.per_cu - 1] + (rest ? per * cd.us[rest - 1] : 0.0);
+      if (sp > 1) t += kSplitUs + 2.0 * sp * M * N * 4 / kPartBytesUs;
       if (t < best_t * 0.999) {
         best_t = t;
-        best = TilePlan{c.bm, c.bn, sp};
+        best = TilePlan{cd.bm, cd.bn, sp};
       }
     }
   }

@@ -459,13 +459,12 @@ BSFP4_API bsfp4_status bsfp4_int8_gated_ffn(const int8_t* A, const float* sa, co
  *   x        device bf16 [M, H], M >= 0
  *   W        device bf16 [2 I, H]: gate rows, then up rows
  *   h        device bf16 [M, I]
- *   gate_up  device bf16 [M, 2 I] or NULL: [G | U] rounded, for the backward
- *            pass
+ *   gate_up  device float [M, 2 I] or NULL: [G | U] for the backward pass
  *   sizes    H > 0, I > 0, multiples of 8, H < 2^22, I < 2^21
  *   ws       bsfp4_gated_ffn_workspace_size(M, I, H) bytes
  *
  * bsfp4_gated_ffn_backward: from dh = dL/dh, with dG = dh U act'(G) and dU =
- *   dh act(G) (FP32 from gate_up, rounded to bf16 for the matrix cores):
+ *   dh act(G) (FP32, rounded to bf16 for the matrix cores):
  *     dx = bf16_rne([dG | dU] W),  dW = bf16_rne([dG | dU]^T x)
  *   dx       device bf16 [M, H] or NULL (not computed)
  *   dW       device bf16 [2 I, H] or NULL (not computed); zeros for M == 0
@@ -474,11 +473,11 @@ BSFP4_API bsfp4_status bsfp4_int8_gated_ffn(const int8_t* A, const float* sa, co
  * ------------------------------------------------------------------------- */
 BSFP4_API size_t bsfp4_gated_ffn_workspace_size(int64_t M, int64_t I, int64_t H);
 BSFP4_API bsfp4_status bsfp4_gated_ffn(const uint16_t* x, const uint16_t* W, int act, uint16_t* h,
-                                       uint16_t* gate_up, int64_t M, int64_t I, int64_t H, void* ws,
+                                       float* gate_up, int64_t M, int64_t I, int64_t H, void* ws,
                                        size_t ws_bytes, void* stream);
 BSFP4_API size_t bsfp4_gated_ffn_backward_workspace_size(int64_t M, int64_t I, int64_t H);
 BSFP4_API bsfp4_status bsfp4_gated_ffn_backward(const uint16_t* dh, const uint16_t* x, const uint16_t* W,
-                                                const uint16_t* gate_up, int act, uint16_t* dx, uint16_t* dW,
+                                                const float* gate_up, int act, uint16_t* dx, uint16_t* dW,
                                                 int64_t M, int64_t I, int64_t H, void* ws, size_t ws_bytes,
                                                 void* stream);
 

@@ -73,11 +73,12 @@ def test_gated():
     refused("unknown activation", bs.gated_ffn, x, W, act=None)
     refused("unknown activation", bs.gated_ffn, x, W, act=["silu"])
     refused("out must have", bs.gated_ffn, x, W, out=m(4, 32))
-    dh, gu = m(4, 16), m(4, 32)
+    dh, gu = m(4, 16), m(4, 32, dtype=F32)
     reaches_device_check(bs.gated_ffn_backward, dh, x, W, gu)
     refused("dh must have", bs.gated_ffn_backward, m(4, 32), x, W, gu)
-    refused("gate_up must have", bs.gated_ffn_backward, dh, x, W, m(4, 16))
-    refused("contiguous", bs.gated_ffn_backward, dh, x, W, m(32, 4).t())
+    refused("gate_up must have", bs.gated_ffn_backward, dh, x, W, m(4, 16, dtype=F32))
+    refused("float32", bs.gated_ffn_backward, dh, x, W, m(4, 32), error=TypeError)
+    refused("contiguous", bs.gated_ffn_backward, dh, x, W, m(32, 4, dtype=F32).t())
 
 
 def test_block_norm():

@@ -39,7 +39,7 @@ def test_forward(M, H, I, act):
     assert (guard[0] == 7).all() and (guard[M + 1] == 7).all()
     h2, gu = bs.gated_ffn(x, W, act=act, save_gate_up=True)
     assert torch.equal(h2, h)
-    R.check(gu, y, e, f"gate_up {M}x{H}x{I}")
+    assert gu.dtype == torch.float32 and ((gu.double() - y).abs() <= e).all()
 
 
 def backward_reference(dh, x, W, gate_up, act):
