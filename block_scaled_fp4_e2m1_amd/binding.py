@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -72,6 +73,10 @@ class BlockNormArgs(ctypes.Structure):
     ]
 
 
+# the same bytes in one call: filling the structure field by field takes 1.5 us longer
+_pack_norm = struct.Struct("@5Qddqqq11Q").pack
+
+
 # name -> (restype, argtypes)
 _SIGNATURES = {
     "bsfp4_version": (ctypes.c_int, []),
@@ -97,9 +102,9 @@ _SIGNATURES = {
     "bsfp4_gated_ffn_backward_workspace_size": (_c_size, [_c_i64, _c_i64, _c_i64]),
     "bsfp4_gated_ffn_backward": (ctypes.c_int, [_c_ptr, _c_ptr, _c_ptr, _c_ptr, ctypes.c_int, _c_ptr, _c_ptr,
                                                 _c_i64, _c_i64, _c_i64, _c_ptr, _c_size, _c_ptr]),
-    "bsfp4_block_norm": (ctypes.c_int, [ctypes.POINTER(BlockNormArgs), _c_ptr]),
+    "bsfp4_block_norm": (ctypes.c_int, [_c_ptr, _c_ptr]),
     "bsfp4_block_norm_backward_workspace_size": (_c_size, [_c_i64, _c_i64, _c_i64]),
-    "bsfp4_block_norm_backward": (ctypes.c_int, [ctypes.POINTER(BlockNormArgs), _c_ptr, _c_size, _c_ptr]),
+    "bsfp4_block_norm_backward": (ctypes.c_int, [_c_ptr, _c_ptr, _c_size, _c_ptr]),
     "fp4_gemm_workspace_size": (_c_size, [ctypes.c_int, _c_i64, _c_i64, _c_i64]),
     "fp4_gemm": (ctypes.c_int, [ctypes.c_int, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr,
                                 _c_i64, _c_i64, _c_i64, _c_ptr, _c_size, _c_ptr]),
@@ -606,8 +611,8 @@ def gated_ffn_backward(dh, x, W13, gate_up, act="silu", need_dx: bool = True, ne
     return dx, dW
 
 
-def _norm_args(x, rows, rows_name, w_post, w_pre, gate, scale, eps) -> BlockNormArgs:
-    """Checks what forward and backward share; `rows` is the [T, H] tensor that is always there."""
+def _norm_args(x, rows, rows_name, w_post, w_pre, gate, eps):
+    """Checks what forward and backward share; `rows` is the [T, H] tensor that is always there.  (T, H, groups)"""
     _need(rows, torch.bfloat16, rows_name)
     _dims(rows, 2, rows_name)
     T, H = rows.shape
@@ -633,13 +638,11 @@ def _norm_args(x, rows, rows_name, w_post, w_pre, gate, scale, eps) -> BlockNorm
             raise ValueError(f"the {T} rows are not a multiple of the {groups} gate rows")
     if not 0.0 < eps < 1e30:
         raise ValueError(f"eps must be positive and finite, got {eps}")
-    return BlockNormArgs(scale=scale, eps=eps, T=T, H=H, groups=groups)
+    return T, H, groups
 
 
-def _fill(a: BlockNormArgs, **tensors):
-    for name, t in tensors.items():
-        if t is not None:
-            setattr(a, name, t.data_ptr())
+def _z(t) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 def block_norm(x, residual, w_post=None, w_pre=None, gate=None, scale: float = 1.0, eps: float = 1e-6,
@@ -654,11 +657,9 @@ def block_norm(x, residual, w_post=None, w_pre=None, gate=None, scale: float = 1
     int8_quantize) or res alone without w_pre.  res_out may be residual (in place)."""
     if fmt not in ("bf16", "int8"):
         raise ValueError(f"unknown output format {fmt!r} (bf16 or int8)")
-    a = _norm_args(x, residual, "residual", w_post, w_pre, gate, scale, eps)
-    T, H = residual.shape
-    if fmt == "int8":
-        if w_pre is None:
-            raise ValueError("fmt='int8' needs w_pre")
+    T, H, groups = _norm_args(x, residual, "residual", w_post, w_pre, gate, eps)
+    if fmt == "int8" and w_pre is None:
+        raise ValueError("fmt='int8' needs w_pre")
     if res_out is not None and x is None:
         raise ValueError("without x nothing is written to res_out")
     _out(res_out, (T, H), torch.bfloat16, "res_out")
@@ -666,17 +667,18 @@ def block_norm(x, residual, w_post=None, w_pre=None, gate=None, scale: float = 1
                   (res_out, "res_out"))
     res = residual
     if x is not None:
-        res = res_out if res_out is not None else torch.empty((T, H), dtype=torch.bfloat16, device=dev)
-        _fill(a, res_out=res)
+        res = res_out if res_out is not None else torch.empty_like(residual)
+    z = q = s = None
     outs = ()
     if w_pre is not None and fmt == "bf16":
-        outs = (torch.empty((T, H), dtype=torch.bfloat16, device=dev),)
-        _fill(a, z=outs[0])
+        z = torch.empty_like(residual)
+        outs = (z,)
     elif w_pre is not None:
-        outs = (torch.empty((T, H), dtype=torch.int8, device=dev), torch.empty(T, dtype=torch.float32, device=dev))
-        _fill(a, q=outs[0], s=outs[1])
-    _fill(a, x=x, residual=residual, w_post=w_post, w_pre=w_pre, gate=gate)
-    _launch(dev, "bsfp4_block_norm", load().bsfp4_block_norm, ctypes.byref(a))
+        q, s = residual.new_empty((T, H), dtype=torch.int8), residual.new_empty(T, dtype=torch.float32)
+        outs = (q, s)
+    args = _pack_norm(_z(x), residual.data_ptr(), _z(w_post), _z(w_pre), _z(gate), scale, eps, T, H, groups,
+                      0 if x is None else res.data_ptr(), _z(z), _z(q), _z(s), 0, 0, 0, 0, 0, 0, 0)
+    _launch(dev, "bsfp4_block_norm", load().bsfp4_block_norm, args)
     return (res, *outs) if outs else res
 
 
@@ -686,8 +688,7 @@ def block_norm_backward(dres, dz, x, res, w_post=None, w_pre=None, gate=None, sc
     zeros; dz None without w_pre), res its first output.  Returns (dx, dresidual, dw_post, dw_pre, dgate), bf16 for the
     rows, float32 for the vectors, None for those that were not given."""
     rows = res if res is not None else dres
-    a = _norm_args(x, rows, "res" if res is not None else "dres", w_post, w_pre, gate, scale, eps)
-    T, H = rows.shape
+    T, H, groups = _norm_args(x, rows, "res" if res is not None else "dres", w_post, w_pre, gate, eps)
     if w_pre is not None and (res is None or dz is None):
         raise ValueError("w_pre needs res and dz")
     if w_pre is None and dz is not None:
@@ -698,15 +699,14 @@ def block_norm_backward(dres, dz, x, res, w_post=None, w_pre=None, gate=None, sc
         _out(t, (T, H), torch.bfloat16, n)
     dev = _device((rows, "res"), (dres, "dres"), (dz, "dz"), (x, "x"), (w_post, "w_post"), (w_pre, "w_pre"),
                   (gate, "gate"))
-    row = lambda: torch.empty((T, H), dtype=torch.bfloat16, device=dev)  # noqa: E731
-    vec = lambda w: None if w is None else torch.empty(w.shape, dtype=torch.float32, device=dev)  # noqa: E731
-    dx, dresidual = (row() if x is not None else None), row()
+    vec = lambda w: None if w is None else torch.empty_like(w, dtype=torch.float32)  # noqa: E731
+    dx, dresidual = (torch.empty_like(rows) if x is not None else None), torch.empty_like(rows)
     dw_post, dw_pre, dgate = vec(w_post), vec(w_pre), vec(gate)
-    _fill(a, x=x, w_post=w_post, w_pre=w_pre, gate=gate, res_out=res, dres_out=dres, dz=dz, dx=dx, dres=dresidual,
-          dw_post=dw_post, dw_pre=dw_pre, dgate=dgate)
+    args = _pack_norm(_z(x), 0, _z(w_post), _z(w_pre), _z(gate), scale, eps, T, H, groups, _z(res), 0, 0, 0, _z(dres),
+                      _z(dz), _z(dx), dresidual.data_ptr(), _z(dw_post), _z(dw_pre), _z(dgate))
     lib = load()
-    _call(dev, "bsfp4_block_norm_backward", lib.bsfp4_block_norm_backward, (ctypes.byref(a),),
-          lib.bsfp4_block_norm_backward_workspace_size, (T, H, a.groups))
+    _call(dev, "bsfp4_block_norm_backward", lib.bsfp4_block_norm_backward, (args,),
+          lib.bsfp4_block_norm_backward_workspace_size, (T, H, groups))
     return dx, dresidual, dw_post, dw_pre, dgate
 
 

@@ -534,6 +534,7 @@ bsfp4::BlockNormArgs norm_args(const bsfp4_block_norm_args* a) {
   p.gate = a->gate;
   p.scale = (float)a->scale;
   p.eps = a->eps;
+  p.inv_h = 1.0 / (double)a->H;
   p.T = a->T;
   p.groups = a->groups;
   p.group_rows = a->T / a->groups;

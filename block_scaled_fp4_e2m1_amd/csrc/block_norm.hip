@@ -33,10 +33,10 @@
 namespace bsfp4 {
 namespace {
 
-// fl32(1 / sqrt(sum / H + eps)): the hardware's 64-bit estimate and two Newton
+// fl32(1 / sqrt(sum inv_h + eps)), inv_h = 1 / H: the hardware's 64-bit estimate and two Newton
 // steps, y (1.5 - 0.5 v y^2), leave an error far below half a 32-bit unit.
-__device__ __forceinline__ float rstd_of(double sum, int H, double eps) {
-  const double v = sum / (double)H + eps;
+__device__ __forceinline__ float rstd_of(double sum, double inv_h, double eps) {
+  const double v = sum * inv_h + eps;
   double y = __builtin_amdgcn_rsq(v);
   if (v < __builtin_inf()) {
 #pragma unroll
@@ -57,13 +57,34 @@ __device__ __forceinline__ uint4 chunk_or_zero(const uint16_t* row, int i, bool 
   return live ? reinterpret_cast<const uint4*>(row)[i] : make_uint4(0, 0, 0, 0);
 }
 
+// A row as a buffer: lanes past its end read zeros and write nothing, and the
+// address is four scalars and a 32-bit lane offset for every array.
+struct RowBuf {
+  __amdgpu_buffer_rsrc_t r;
+  __device__ __forceinline__ RowBuf(const uint16_t* p, int64_t m, int H, bool live = true)
+      : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p) + m * H, (short)0, live ? 2 * H : 0, 0x00020000)) {}
+  __device__ __forceinline__ uint4 load(int i) const {
+    return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, i * 16, 0, 0));
+  }
+  __device__ __forceinline__ void store(int i, const uint4& v) const {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    __builtin_amdgcn_raw_buffer_store_b128(u32x4{v.x, v.y, v.z, v.w}, r, i * 16, 0, 0);
+  }
+};
+
+// Keeps a chunk packed: unpacked copies of loop invariants would cost twice the
+// registers (and a workgroup per compute unit in the backward pass).
+__device__ __forceinline__ void keep_packed(uint4& c) {
+  asm volatile("" : "+v"(c.x), "+v"(c.y), "+v"(c.z), "+v"(c.w));
+}
+
 template <int NT, int CH, bool kInt8>
 __global__ void __launch_bounds__(NT < 256 ? 256 : NT)
     block_norm_fwd(const BlockNormArgs p) {
   constexpr int kRows = NT < 256 ? 256 / NT : 1;
   static_assert(kRows == 1 || NT == 64, "several rows per workgroup: a wave each");
   __shared__ double red[2][NT / 64];
-  __shared__ uint32_t redm[NT / 64];
+  __shared__ int redm[NT / 64];
   const int t = kRows > 1 ? (int)(threadIdx.x % NT) : (int)threadIdx.x;
   const int64_t m = (int64_t)blockIdx.x * kRows + (kRows > 1 ? threadIdx.x / NT : 0);
   if (m >= p.T) return;
@@ -87,7 +108,7 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT)
 #pragma unroll
       for (int j = 0; j < CH; j++) s[0] = sumsq8(x[j], s[0]);
       row_sum<NT>(s, red[0]);
-      xs = rstd_of(s[0], H, p.eps);
+      xs = rstd_of(s[0], p.inv_h, p.eps);
     }
 #pragma unroll
     for (int j = 0; j < CH; j++) {
@@ -112,7 +133,7 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT)
 #pragma unroll
   for (int j = 0; j < CH; j++) s[0] = sumsq8(r[j], s[0]);
   row_sum<NT>(s, red[1]);
-  const float rs = rstd_of(s[0], H, p.eps);
+  const float rs = rstd_of(s[0], p.inv_h, p.eps);
   uint32_t mx = 0;
 #pragma unroll
   for (int j = 0; j < CH; j++) {
@@ -145,15 +166,15 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT)
 // vector gradients in registers.  Strips are either 1 / S of a gate group (the
 // group's dgate is then summed over S partials), or whole groups (its dgate is
 // final).  CH 16-byte chunks per thread: 1 up to H = 8 NT.
-template <int NT, int CH>
-__global__ void __launch_bounds__(NT)
+template <int NT, int CH, bool kAll>
+__global__ void __launch_bounds__(NT, 4)
     block_norm_bwd(const BlockNormArgs p) {
   __shared__ double red_a[3 * (NT / 64)];
   __shared__ double red_b[NT / 64];
   const int t = threadIdx.x;
   const int H = p.H, chunks = H / 8;
-  const bool has_x = p.x != nullptr, has_post = p.w_post != nullptr, has_pre = p.w_pre != nullptr,
-             has_gate = p.gate != nullptr, has_dres = p.dres_out != nullptr;
+  const bool has_x = kAll || p.x != nullptr, has_post = kAll || p.w_post != nullptr, has_pre = kAll || p.w_pre != nullptr,
+             has_gate = kAll || p.gate != nullptr, has_dres = kAll || p.dres_out != nullptr;
   const int64_t strip = blockIdx.x;
   int64_t g0, g1, part = 0, parts = 1;
   if (p.strips_per_group > 1) {
@@ -166,38 +187,41 @@ __global__ void __launch_bounds__(NT)
     g1 = min(g0 + p.groups_per_strip, p.groups);
   }
   float apost[CH][8] = {}, apre[CH][8] = {};
-  uint4 wp[CH], wn[CH];
+  // Two chunks per thread leave no registers for a row ahead nor for the vectors,
+  // which are then read again with every row (from the caches).
+  constexpr bool kAhead = CH == 1;
+  uint4 wp[CH] = {}, wn[CH] = {}, gt[CH] = {};
+  auto vectors = [&](int64_t g) {
 #pragma unroll
-  for (int j = 0; j < CH; j++) {
-    const int i = t + j * NT;
-    if (has_post) wp[j] = chunk_or_zero(p.w_post, i, i < chunks);
-    if (has_pre) wn[j] = chunk_or_zero(p.w_pre, i, i < chunks);
-  }
+    for (int j = 0; j < CH; j++) {
+      const int i = t + j * NT;
+      if (has_post) wp[j] = RowBuf(p.w_post, 0, H).load(i);
+      if (has_pre) wn[j] = RowBuf(p.w_pre, 0, H).load(i);
+      if (has_gate) gt[j] = RowBuf(p.gate, g, H).load(i);
+    }
+  };
   for (int64_t g = g0; g < g1; g++) {
     const int64_t ra = g * p.group_rows + p.group_rows * part / parts;
     const int64_t rb = g * p.group_rows + p.group_rows * (part + 1) / parts;
     float agate[CH][8] = {};
-    uint4 gt[CH];
-#pragma unroll
-    for (int j = 0; j < CH; j++) {
-      const int i = t + j * NT;
-      if (has_gate) gt[j] = chunk_or_zero(p.gate + g * H, i, i < chunks);
-    }
+    if (kAhead) vectors(g);
     uint4 nx[CH], nr[CH], nz[CH], nd[CH];  // the next row's chunks
     auto load = [&](int64_t m) {
-      const int64_t off = m * H;
 #pragma unroll
       for (int j = 0; j < CH; j++) {
         const int i = t + j * NT;
-        const bool live = i < chunks && m < rb;
-        if (has_x) nx[j] = chunk_or_zero(p.x + off, i, live);
-        if (has_pre) nr[j] = chunk_or_zero(p.res + off, i, live);
-        if (has_pre) nz[j] = chunk_or_zero(p.dz + off, i, live);
-        if (has_dres) nd[j] = chunk_or_zero(p.dres_out + off, i, live);
+        if (has_x) nx[j] = RowBuf(p.x, m, H, m < rb).load(i);
+        if (has_pre) nr[j] = RowBuf(p.res, m, H, m < rb).load(i);
+        if (has_pre) nz[j] = RowBuf(p.dz, m, H, m < rb).load(i);
+        if (has_dres) nd[j] = RowBuf(p.dres_out, m, H, m < rb).load(i);
       }
     };
-    load(ra);
+    if (kAhead) load(ra);
     for (int64_t m = ra; m < rb; m++) {
+      if (!kAhead) {
+        load(m);
+        vectors(g);
+      }
       uint4 x[CH], r[CH], z[CH], d4[CH];
 #pragma unroll
       for (int j = 0; j < CH; j++) {
@@ -205,8 +229,11 @@ __global__ void __launch_bounds__(NT)
         r[j] = nr[j];
         z[j] = nz[j];
         d4[j] = nd[j];
+        keep_packed(wp[j]);
+        keep_packed(wn[j]);
+        keep_packed(gt[j]);
       }
-      load(m + 1);
+      if (kAhead) load(m + 1);
       double s[3] = {0.0, 0.0, 0.0};
 #pragma unroll
       for (int j = 0; j < CH; j++) {
@@ -222,14 +249,20 @@ __global__ void __launch_bounds__(NT)
           s[2] += (double)dot;
         }
       }
+      __builtin_amdgcn_sched_barrier(0);
       row_sum<NT>(s, red_a);
-      const float xs = has_x && has_post ? rstd_of(s[0], H, p.eps) : 1.0f;
-      const float rs = has_pre ? rstd_of(s[1], H, p.eps) : 1.0f;
-      const float mz = (float)(s[2] / (double)H * (double)rs);  // mean(gz zh)
+      __builtin_amdgcn_sched_barrier(0);
+      const float xs = has_x && has_post ? rstd_of(s[0], p.inv_h, p.eps) : 1.0f;
+      const float rs = has_pre ? rstd_of(s[1], p.inv_h, p.eps) : 1.0f;
+      const float mz = (float)(s[2] * p.inv_h) * rs;  // mean(gz zh)
       float d[CH][8];
       double sb[1] = {0.0};
 #pragma unroll
       for (int j = 0; j < CH; j++) {
+        keep_packed(x[j]);
+        keep_packed(r[j]);
+        keep_packed(z[j]);
+        keep_packed(wn[j]);
         float rv[8], zv[8], wv[8];
         if (has_dres) {
           unpack8(d4[j], d[j]);
@@ -249,7 +282,7 @@ __global__ void __launch_bounds__(NT)
           }
         }
         const int i = t + j * NT;
-        if (i < chunks && p.dres) reinterpret_cast<uint4*>(p.dres + m * H)[i] = pack8(d[j]);
+        RowBuf(p.dres, m, H).store(i, pack8(d[j]));
         if (has_x) {
           float xv[8], pv[8], gv[8], dot = 0.0f;
           unpack8(x[j], xv);
@@ -271,19 +304,21 @@ __global__ void __launch_bounds__(NT)
       if (has_x) {
         float mx = 0.0f;  // mean(gx xh) xs
         if (has_post) {
+          __builtin_amdgcn_sched_barrier(0);
           row_sum<NT>(sb, red_b);
-          mx = (float)(sb[0] / (double)H * (double)xs);
+          __builtin_amdgcn_sched_barrier(0);
+          mx = (float)(sb[0] * p.inv_h) * xs;
         }
 #pragma unroll
         for (int j = 0; j < CH; j++) {
+          keep_packed(x[j]);
           if (has_post) {
             float xv[8];
             unpack8(x[j], xv);
 #pragma unroll
             for (int k = 0; k < 8; k++) d[j][k] = xs * (d[j][k] - xv[k] * xs * mx);
           }
-          const int i = t + j * NT;
-          if (i < chunks) reinterpret_cast<uint4*>(p.dx + m * H)[i] = pack8(d[j]);
+          RowBuf(p.dx, m, H).store(t + j * NT, pack8(d[j]));
         }
       }
     }
@@ -317,10 +352,11 @@ __global__ void __launch_bounds__(NT)
 }
 
 // out[h] = sum over strips of part[strip][h], in a fixed order: workgroups of 64
-// columns x 16 strip lanes.  blockIdx.y: 0 dw_post, 1 dw_pre, 2 + g dgate of group g.
+// columns, 16 threads of four columns each on every 64th strip.  blockIdx.y: 0
+// dw_post, 1 dw_pre, 2 + g dgate of group g.
 __global__ void __launch_bounds__(1024)
     block_norm_sum(const BlockNormArgs p, int64_t strips) {
-  __shared__ float red[16][64];
+  __shared__ __attribute__((aligned(16))) float red[64][64];
   const int which = blockIdx.y;
   const float* src;
   float* dst;
@@ -337,20 +373,28 @@ __global__ void __launch_bounds__(1024)
     dst = p.dgate ? p.dgate + (int64_t)(which - 2) * p.H : nullptr;
   }
   if (src == nullptr) return;
-  const int c = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int h = blockIdx.x * 64 + c;
-  float acc = 0.0f;
-  if (h < p.H) {
+  const int c4 = threadIdx.x & 15, w = threadIdx.x >> 4;
+  const int h = blockIdx.x * 64 + c4 * 4;
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (h < p.H) {  // H % 8 == 0: four columns are in or out together
 #pragma unroll 4
-    for (int64_t s = w; s < n; s += 16) acc += src[s * p.H + h];
+    for (int64_t s = w; s < n; s += 64) {
+      const float4 v = *reinterpret_cast<const float4*>(src + s * p.H + h);
+      acc = make_float4(acc.x + v.x, acc.y + v.y, acc.z + v.z, acc.w + v.w);
+    }
   }
-  red[w][c] = acc;
+  *reinterpret_cast<float4*>(&red[w][c4 * 4]) = acc;
+  const int c = threadIdx.x & 63, k = threadIdx.x >> 6;
   __syncthreads();
-  if (w == 0 && h < p.H) {
-    float v = red[0][c];
+  const float v = (red[k][c] + red[k + 16][c]) + (red[k + 32][c] + red[k + 48][c]);
+  __syncthreads();
+  red[k][c] = v;
+  __syncthreads();
+  if (k == 0 && blockIdx.x * 64 + c < p.H) {
+    float t = red[0][c];
 #pragma unroll
-    for (int i = 1; i < 16; i++) v += red[i][c];
-    dst[h] = v;
+    for (int i = 1; i < 16; i++) t += red[i][c];
+    dst[blockIdx.x * 64 + c] = t;
   }
 }
 
@@ -358,9 +402,23 @@ struct Strips {
   int64_t per_group, groups_per_strip, count;
 };
 
-// Strips of about 16 rows or more, at most ~2 workgroups of 512 threads per CU.
-Strips plan_strips(int64_t T, int64_t groups) {
-  const int64_t want = std::min<int64_t>(512, std::max<int64_t>(1, (T + 15) / 16));
+// Threads of a row in the backward pass: one chunk each up to H = 8192, else two.
+int bwd_threads(int64_t H) {
+  const int64_t chunks = H / 8;
+  int nt = 64;
+  while (nt < 1024 && nt < chunks) nt *= 2;
+  return nt;
+}
+
+// As many strips as workgroups are resident at once (16 waves of 128 registers per
+// compute unit), at most one per row: a row's two reductions cost some 2 us of
+// latency, so few rows are spread wide; past one per compute unit a strip takes
+// four rows, as its partial vectors cost the bytes of one.  More than 1024 strips cost more in the sum
+// of their vectors than they save (4000 x 512 with 4000 strips 38 us, with 250 25).
+Strips plan_strips(int64_t T, int64_t H, int64_t groups) {
+  const int64_t resident = std::min<int64_t>(1024, (int64_t)device_cu_count() * (1024 / bwd_threads(H)));
+  const int64_t cus = device_cu_count();
+  const int64_t want = std::min<int64_t>(resident, std::max<int64_t>(std::max<int64_t>(1, std::min(T, cus)), T / 4));
   const int64_t rows = T / groups;
   Strips s;
   if (groups >= want) {
@@ -378,7 +436,7 @@ Strips plan_strips(int64_t T, int64_t groups) {
 }  // namespace
 
 size_t block_norm_bwd_workspace(int64_t T, int64_t H, int64_t groups) {
-  return (size_t)plan_strips(T, groups).count * H * 3 * sizeof(float);
+  return (size_t)plan_strips(T, H, groups).count * H * 3 * sizeof(float);
 }
 
 hipError_t launch_block_norm(const BlockNormArgs& p, hipStream_t stream) {
@@ -391,9 +449,16 @@ hipError_t launch_block_norm(const BlockNormArgs& p, hipStream_t stream) {
     else                                                                                               \
       block_norm_fwd<NT, CH, false><<<grid, NT < 256 ? 256 : NT, 0, stream>>>(p);                      \
   } while (0)
+  // Many rows: two chunks per thread keep more bytes in flight (8192 x 4096 40.6 us
+  // against 45.2 with one, 4000 x 7168 36.5 against 43.0); few rows or short ones: one
+  // chunk, more threads, less latency (1 x 4096 3.5 against 4.5, 1024 x 2048 5.9
+  // against 6.6).
+  const bool many = p.T >= 1024;
   if (chunks <= 64) BSFP4_FWD(64, 1);
   else if (chunks <= 256) BSFP4_FWD(256, 1);
+  else if (chunks <= 512 && many) BSFP4_FWD(256, 2);
   else if (chunks <= 512) BSFP4_FWD(512, 1);
+  else if (chunks <= 1024 && many) BSFP4_FWD(512, 2);
   else if (chunks <= 1024) BSFP4_FWD(1024, 1);
   else BSFP4_FWD(1024, 2);
 #undef BSFP4_FWD
@@ -401,7 +466,7 @@ hipError_t launch_block_norm(const BlockNormArgs& p, hipStream_t stream) {
 }
 
 hipError_t launch_block_norm_bwd(BlockNormArgs p, float* ws, hipStream_t stream) {
-  const Strips s = plan_strips(p.T, p.groups);
+  const Strips s = plan_strips(p.T, p.H, p.groups);
   p.strips_per_group = s.per_group;
   p.groups_per_strip = s.groups_per_strip;
   const size_t n = (size_t)s.count * p.H;
@@ -410,12 +475,22 @@ hipError_t launch_block_norm_bwd(BlockNormArgs p, float* ws, hipStream_t stream)
   p.part_gate = p.gate && s.per_group > 1 ? ws + 2 * n : nullptr;
   const int chunks = p.H / 8;
   const unsigned grid = (unsigned)s.count;
-  if (chunks <= 64) block_norm_bwd<64, 1><<<grid, 64, 0, stream>>>(p);
-  else if (chunks <= 128) block_norm_bwd<128, 1><<<grid, 128, 0, stream>>>(p);
-  else if (chunks <= 256) block_norm_bwd<256, 1><<<grid, 256, 0, stream>>>(p);
-  else if (chunks <= 512) block_norm_bwd<512, 1><<<grid, 512, 0, stream>>>(p);
-  else if (chunks <= 1024) block_norm_bwd<1024, 1><<<grid, 1024, 0, stream>>>(p);
-  else block_norm_bwd<1024, 2><<<grid, 1024, 0, stream>>>(p);
+  const bool all = p.x && p.w_post && p.w_pre && p.gate && p.dres_out && p.T > 0;
+#define BSFP4_BWD(NT, CH)                                        \
+  do {                                                           \
+    if (all) block_norm_bwd<NT, CH, true><<<grid, NT, 0, stream>>>(p); \
+    else block_norm_bwd<NT, CH, false><<<grid, NT, 0, stream>>>(p);    \
+  } while (0)
+  switch (bwd_threads(p.H)) {
+    case 64: BSFP4_BWD(64, 1); break;
+    case 128: BSFP4_BWD(128, 1); break;
+    case 256: BSFP4_BWD(256, 1); break;
+    case 512: BSFP4_BWD(512, 1); break;
+    default:
+      if (chunks <= 1024) BSFP4_BWD(1024, 1);
+      else BSFP4_BWD(1024, 2);
+  }
+#undef BSFP4_BWD
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (!p.part_post && !p.part_pre && !p.part_gate) return hipSuccess;

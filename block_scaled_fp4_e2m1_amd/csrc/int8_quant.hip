@@ -25,7 +25,7 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT)
     int8_quant_rows(const uint16_t* __restrict__ x, int64_t M, int K, int8_t* __restrict__ q,
                     float* __restrict__ s) {
   constexpr int kRows = NT < 256 ? 256 / NT : 1;
-  __shared__ uint32_t red[NT / 64];
+  __shared__ int red[NT / 64];
   const int t = kRows > 1 ? (int)(threadIdx.x % NT) : (int)threadIdx.x;
   const int64_t m = (int64_t)blockIdx.x * kRows + (kRows > 1 ? threadIdx.x / NT : 0);
   if (m >= M) return;  // a whole wave (rows shared by several waves fill the grid exactly)

@@ -43,46 +43,78 @@ __device__ __forceinline__ uint32_t amax_bits8(const uint4& c, uint32_t m) {
   return m;
 }
 
-// Sum of N doubles over the NT threads that hold one row (NT 64: a wave of its
-// own, no barrier; else the whole workgroup).  The waves' sums are added in
-// wave order, so every thread gets the same bits on every call.  `red` holds
-// N * NT / 64 doubles and must not be in use by an earlier call still being
-// read: callers alternate two buffers.
-template <int NT, int N>
-__device__ __forceinline__ void row_sum(double (&v)[N], double* red) {
+// A value of another lane of the wave: neighbours at 1, 2 (lane xor) and at the
+// mirrored places of 8 and 16 lanes by a data-parallel move, 16 and 32 apart
+// through LDS hardware.  Combining with all six in turn gives every lane the same
+// bits (both partners of a step form the same pair).
+template <int kStep>
+__device__ __forceinline__ int lane_partner(int v) {
+  if constexpr (kStep == 0) return __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, true);        // xor 1
+  else if constexpr (kStep == 1) return __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, true);   // xor 2
+  else if constexpr (kStep == 2) return __builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, true);  // mirror of 8
+  else if constexpr (kStep == 3) return __builtin_amdgcn_mov_dpp(v, 0x140, 0xF, 0xF, true);  // mirror of 16
+  else return __shfl_xor(v, kStep == 4 ? 16 : 32, 64);
+}
+template <int kStep>
+__device__ __forceinline__ double lane_partner(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)lane_partner<kStep>((int)(uint32_t)u);
+  const uint32_t hi = (uint32_t)lane_partner<kStep>((int)(uint32_t)(u >> 32));
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+struct AddOp {
+  __device__ __forceinline__ double operator()(double a, double b) const { return a + b; }
+};
+struct MaxOp {
+  __device__ __forceinline__ int operator()(int a, int b) const { return max(a, b); }
+};
+
+// Over groups of 2^kSteps lanes (64 with all six steps).
+template <int kSteps, class Op, class T>
+__device__ __forceinline__ T lanes_reduce(T v, Op op) {
+  if constexpr (kSteps > 0) v = op(v, lane_partner<0>(v));
+  if constexpr (kSteps > 1) v = op(v, lane_partner<1>(v));
+  if constexpr (kSteps > 2) v = op(v, lane_partner<2>(v));
+  if constexpr (kSteps > 3) v = op(v, lane_partner<3>(v));
+  if constexpr (kSteps > 4) v = op(v, lane_partner<4>(v));
+  if constexpr (kSteps > 5) v = op(v, lane_partner<5>(v));
+  return v;
+}
+
+constexpr int log2_of(int n) { return n <= 1 ? 0 : 1 + log2_of(n / 2); }
+
+// N values over the NT threads that hold one row (NT 64: a wave of its own, no
+// barrier; else the whole workgroup), every thread with the same bits.  The waves'
+// values meet in `red` (N NT / 64 of them), where each group of NT / 64 lanes
+// combines them: one value in a register at a time.  `red` must not be in use by
+// an earlier call still being read: two calls that alternate use two buffers.
+template <int NT, class Op, class T, int N>
+__device__ __forceinline__ void row_reduce(T (&v)[N], T* red, Op op) {
+  constexpr int W = NT / 64;
+  static_assert((W & (W - 1)) == 0 && W <= 16, "waves of a row");
 #pragma unroll
-  for (int k = 0; k < N; k++)
+  for (int k = 0; k < N; k++) v[k] = lanes_reduce<6>(v[k], op);
+  if constexpr (W > 1) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if (lane == 0) {
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v[k] += __shfl_xor(v[k], o, 64);
-  if constexpr (NT > 64) {
-    const int wave = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0) {
-#pragma unroll
-      for (int k = 0; k < N; k++) red[wave * N + k] = v[k];
+      for (int k = 0; k < N; k++) red[k * W + wave] = v[k];
     }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < N; k++) {
-      double s = red[k];
-#pragma unroll
-      for (int w = 1; w < NT / 64; w++) s += red[w * N + k];
-      v[k] = s;
-    }
+    for (int k = 0; k < N; k++) v[k] = lanes_reduce<log2_of(W)>(red[k * W + (lane & (W - 1))], op);
   }
 }
 
+template <int NT, int N>
+__device__ __forceinline__ void row_sum(double (&v)[N], double* red) { row_reduce<NT>(v, red, AddOp{}); }
+
 template <int NT>
-__device__ __forceinline__ uint32_t row_max(uint32_t m, uint32_t* red) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
-  if constexpr (NT > 64) {
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
-    __syncthreads();
-    m = red[0];
-#pragma unroll
-    for (int w = 1; w < NT / 64; w++) m = max(m, red[w]);
-  }
-  return m;
+__device__ __forceinline__ uint32_t row_max(uint32_t m, int* red) {
+  int v[1] = {(int)m};
+  row_reduce<NT>(v, red, MaxOp{});
+  return (uint32_t)v[0];
 }
 
 // Per-token 8-bit rounding of a row of bf16 values with largest magnitude amax:

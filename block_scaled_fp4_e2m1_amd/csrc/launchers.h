@@ -147,7 +147,7 @@ struct BlockNormArgs {
   const uint16_t* w_pre;     // [H] or null
   const uint16_t* gate;      // [groups, H] or null
   float scale;
-  double eps;
+  double eps, inv_h;         // inv_h = 1 / H
   int64_t T, groups, group_rows;  // group_rows = T / groups
   int H;
   uint16_t* res_out;  // forward: r' [T, H]
