@@ -15,8 +15,8 @@
 // no transposed copy is ever written.
 //
 // Structure: a BM x BN tile per workgroup of WGM x WGN waves, K in stages of 128
-// bytes per row, two LDS slots filled by direct-to-LDS buffer loads (1 KB each),
-// the next stage's loads in flight while a stage is multiplied.
+// bytes per row, RING LDS slots filled by direct-to-LDS buffer loads (1 KB each),
+// the loads of the RING - 1 stages that follow in flight while a stage is multiplied.
 // LDS layout of a stage, A first:
 //   rows along K   [rows][8 chunks of 16 B], chunk c of row r at position
 //                  c ^ ((r ^ r / 8) & 7): the 32 rows of a fragment read hit
@@ -239,17 +239,17 @@ struct TileArgs {
   void* part;          // splits > 1: float / int32 [splits][M][N or 2 N]
 };
 
-template <int BM, int BN>
+template <int BM, int BN, int RING>
 constexpr int tile_smem() {
-  const int ring = 2 * (BM + BN) * kTileStage;
+  const int ring = RING * (BM + BN) * kTileStage;
   const int out = BM * (BN * 2 + 16);
   return ring > out ? ring : out;
 }
 
 // Waves per SIMD that the LDS lets in: what the registers are sized for.
-template <int BM, int BN, int WAVES>
+template <int BM, int BN, int RING, int WAVES>
 constexpr int tile_waves_simd() {
-  const int w = 160 * 1024 / tile_smem<BM, BN>() * WAVES / 4;
+  const int w = 160 * 1024 / tile_smem<BM, BN, RING>() * WAVES / 4;
   return w < 1 ? 1 : w;
 }
 
@@ -272,17 +272,18 @@ __device__ __forceinline__ void tile_item(const TileArgs& p, int& tile_m, int& t
   tile_n = in_band / rows;
 }
 
-template <bool kInt8, int BM, int BN, int WGM, int WGN, bool kTransA, bool kTransB, int EPI>
-__global__ void __launch_bounds__(64 * WGM * WGN, (tile_waves_simd<BM, BN, WGM * WGN>()))
+template <bool kInt8, int BM, int BN, int WGM, int WGN, int RING, bool kTransA, bool kTransB, int EPI>
+__global__ void __launch_bounds__(64 * WGM * WGN, (tile_waves_simd<BM, BN, RING, WGM * WGN>()))
     tile_gemm(const TileArgs p) {
   typedef Mma<kInt8> MM;
   constexpr int NT = 64 * WGM * WGN, WAVES = WGM * WGN;
   constexpr int WM = BM / WGM, WN = BN / WGN, TM = WM / 32, TN = WN / 32;
   constexpr int kStageA = BM * kTileStage, kStage = (BM + BN) * kTileStage;
   constexpr bool kGated = EPI == kTileGated;
+  static_assert(RING >= 2 && RING <= 4, "ring depth");
   static_assert(!kGated || TN % 2 == 0, "a wave holds gate / up block pairs");
   static_assert(!kInt8 || (!kTransA && !kTransB), "8-bit operands have their rows along K");
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[tile_smem<BM, BN>()];
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[tile_smem<BM, BN, RING>()];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WGN, wn = wave % WGN, g = lane >> 5, lr = lane & 31;
@@ -338,21 +339,23 @@ __global__ void __launch_bounds__(64 * WGM * WGN, (tile_waves_simd<BM, BN, WGM *
     rsa = la.stage_rsrc((int64_t)st * kTileStageK, kend_a - (int64_t)st * kTileStageK);
     rsb = lb.stage_rsrc((int64_t)st * kTileStageK, kend_b - (int64_t)st * kTileStageK);
   };
-  auto issue_one = [&](int j, int st) {
-    const uint32_t slot = lds0 + (uint32_t)(st & 1) * kStage;
+  auto issue_one = [&](int j, int st, int in) {  // load j of stage st into slot `in`
+    const uint32_t slot = lds0 + (uint32_t)in * kStage;
     if (j < decltype(la)::kLoads) la.issue(j, st, rsa, slot);
     else lb.issue(j - decltype(la)::kLoads, st, rsb, slot + kStageA);
   };
-  auto arrive = [&] {
+  // `flying`: stages after the next one whose loads may still be under way
+  auto arrive = [&](auto flying) {
     // this wave's loads of the next stage and its last reads of this one
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(decltype(flying)::value * kIssues) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
-  // kNext: a stage follows;  kAfter: two do
-  auto group = [&](auto next_c, auto after_c, int kk, int st) {
-    constexpr bool kNext = decltype(next_c)::value, kAfter = decltype(after_c)::value;
-    if (kAfter && kk == 3) begin_issue(st + 2);
+  // kLeft: stages that follow (RING: that many or more, so stage st + RING is issued)
+  auto group = [&](auto left_c, int kk, int st, int slot) {
+    constexpr int kLeft = decltype(left_c)::value;
+    constexpr bool kNext = kLeft > 0, kAfter = kLeft >= RING;
+    if (kAfter && kk == 3) begin_issue(st + RING);
 #pragma unroll
     for (int t = 0; t < kMfma; t++) {
       const int i = t / TN, j = t % TN;
@@ -362,39 +365,61 @@ __global__ void __launch_bounds__(64 * WGM * WGN, (tile_waves_simd<BM, BN, WGM *
       if (kk < 3 || kNext) {
 #pragma unroll
         for (int r = 0; r < kReads; r++)
-          if (r * (kMfma / 4) / kReads == t) read_one(r, (st + (kk == 3)) & 1, (kk + 1) & 3, (kk + 1) & 1);
+          if (r * (kMfma / 4) / kReads == t) read_one(r, kk < 3 ? slot : slot + 1 == RING ? 0 : slot + 1, (kk + 1) & 3, (kk + 1) & 1);
       }
-      if (kNext && kk == 2 && t == kMfma * 3 / 4 - 1) arrive();
+      if (kNext && kk == 2 && t == (kMfma > 1 ? kMfma * 3 / 4 - 1 : 0))
+        arrive(std::integral_constant<int, kLeft < RING ? kLeft - 1 : RING - 2>{});
       if (kAfter && kk == 3) {
 #pragma unroll
         for (int l = 0; l < kIssues; l++)
-          if (l * kMfma / kIssues == t) issue_one(l, st + 2);
+          if (l * kMfma / kIssues == t) issue_one(l, st + RING, slot);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  auto stage = [&](auto next_c, auto after_c, int st) {
-    group(next_c, after_c, 0, st);
-    group(next_c, after_c, 1, st);
-    group(next_c, after_c, 2, st);
-    group(next_c, after_c, 3, st);
+  auto stage = [&](auto left_c, int st, int slot) {
+    group(left_c, 0, st, slot);
+    group(left_c, 1, st, slot);
+    group(left_c, 2, st, slot);
+    group(left_c, 3, st, slot);
   };
-  if (s0 < s1) {
-    begin_issue(s0);
+  const int nst = s1 - s0;
+  if (nst > 0) {
 #pragma unroll
-    for (int l = 0; l < kIssues; l++) issue_one(l, s0);
-    arrive();
-    if (s0 + 1 < s1) {
-      begin_issue(s0 + 1);
+    for (int r = 0; r < RING; r++)
+      if (r < nst) {
+        begin_issue(s0 + r);
 #pragma unroll
-      for (int l = 0; l < kIssues; l++) issue_one(l, s0 + 1);
+        for (int l = 0; l < kIssues; l++) issue_one(l, s0 + r, r);
+      }
+    // the first stage has landed when the loads after it are all that is out
+    if (nst >= RING) arrive(std::integral_constant<int, RING - 1>{});
+    else arrive(std::integral_constant<int, 0>{});
+#pragma unroll
+    for (int r = 0; r < kReads; r++) read_one(r, 0, 0, 0);
+    int st = s0, slot = 0;
+    auto advance = [&] {
+      st++;
+      slot = slot + 1 == RING ? 0 : slot + 1;
+    };
+    for (; st + RING < s1; advance()) stage(std::integral_constant<int, RING>{}, st, slot);
+    if constexpr (RING > 3) {
+      if (st + 3 < s1) {
+        stage(std::integral_constant<int, 3>{}, st, slot);
+        advance();
+      }
     }
-#pragma unroll
-    for (int r = 0; r < kReads; r++) read_one(r, s0 & 1, 0, 0);
-    int st = s0;
-    for (; st + 2 < s1; st++) stage(std::true_type{}, std::true_type{}, st);
-    if (st + 1 < s1) stage(std::true_type{}, std::false_type{}, st++);
-    stage(std::false_type{}, std::false_type{}, st);
+    if constexpr (RING > 2) {
+      if (st + 2 < s1) {
+        stage(std::integral_constant<int, 2>{}, st, slot);
+        advance();
+      }
+    }
+    if (st + 1 < s1) {
+      stage(std::integral_constant<int, 1>{}, st, slot);
+      advance();
+    }
+    stage(std::integral_constant<int, 0>{}, st, slot);
   }
 
   // register 4q + e of block (i, j): row wm*WM + 32 i + lr, tile column wn*WN + 32 j + 8q + 4g + e
@@ -494,7 +519,7 @@ __global__ void __launch_bounds__(64 * WGM * WGN, (tile_waves_simd<BM, BN, WGM *
     if constexpr (!kInt8) {
       if (p.gate_up) {  // the sums as they are, gate then up, in whole row segments as well
         constexpr int kPitch4 = kCols * 4 + 16;
-        static_assert(BM * kPitch4 <= tile_smem<BM, BN>(), "a binary32 half tile fits in LDS");
+        static_assert(BM * kPitch4 <= tile_smem<BM, BN, RING>(), "a binary32 half tile fits in LDS");
 #pragma unroll
         for (int half = 0; half < 2; half++) {
           __syncthreads();
@@ -576,42 +601,51 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---- planning --------------------------------------------------------------
+// The kernels of a product.  A large tile does the most with each byte in LDS; a
+// small one with more slots has more loads under way per multiplied stage, which is
+// what a product of few workgroups waits for.
+enum TileKind { kTile256, kTile128, kTile128Deep, kTile64x128, kTile64, kTileKinds };
+
 struct TilePlan {
-  int bm, bn, splits;
+  TileKind kind;
+  int splits;
 };
 
-// Tile shape and K split of an M x N (x K bytes) product: the pair with the least
-// estimated time.  A compute unit holds one 256 x 256 workgroup, two of 128 x 128
-// or three of 64 x 128; a stage takes a workgroup us[c - 1] microseconds when c
-// share the unit, a workgroup's start and end cost kRoundUs, a split's second
-// kernel kSplitUs and its partials their bytes.  The figures are a least-squares
-// fit to 460 timed (shape, tile, split) combinations, M 32 .. 1024, weights of 1536 x
-// 2048 .. 14336 x 4096, bf16 and int8 (10 % rms); the plan's choice is 3 % slower
-// than the best of each shape on average.  N counts weight rows (gated: both
-// halves).
+// Kernel and K split of an M x N (x K bytes) product: the pair with the least
+// estimated time.  A stage takes a workgroup us[c - 1] microseconds when c share a
+// compute unit, its start and end round_us; a split's second kernel costs kSplitUs
+// and its partials their bytes.  The figures are a least-squares fit to 2034 timed
+// (shape, kernel, split) combinations, M 48 .. 4096, weights of 1536 x 2048 .. 14336 x
+// 4096, bf16 and int8 (9 % rms); the plan's choice is 0.8 % slower than the best of
+// each shape on average, 11 % at worst.  N counts weight rows (gated: both halves).
+struct TileCost {
+  int bm, bn, per_cu;
+  double us[2], round_us;
+};
+constexpr TileCost kTileCosts[kTileKinds] = {{256, 256, 1, {1.06, 0}, 5.3},
+                                             {128, 128, 2, {0.59, 0.83}, 2.6},
+                                             {128, 128, 1, {0.50, 0}, 3.2},
+                                             {64, 128, 2, {0.31, 0.56}, 3.3},
+                                             {64, 64, 2, {0.265, 0.36}, 3.1}};
+
 inline TilePlan plan_tile(int64_t M, int64_t N, int64_t kbytes, int cus) {
-  struct Cand {
-    int bm, bn, per_cu;
-    double us[3];
-  };
-  static constexpr Cand cands[] = {{256, 256, 1, {1.06, 0, 0}}, {128, 128, 2, {0.60, 0.80, 0}}, {64, 128, 3, {0.52, 0.64, 0.73}}};
-  static constexpr double kRoundUs[] = {3.9, 2.2, 2.1}, kSplitUs = 2.8, kPartBytesUs = 4.5e6;
+  constexpr double kSplitUs = 3.0, kPartBytesUs = 4.8e6;
   const int64_t stages = (kbytes + kTileStage - 1) / kTileStage;
-  TilePlan best{256, 256, 1};
+  TilePlan best{kTile256, 1};
   double best_t = 1e300;
-  for (int c = 0; c < 3; c++) {
-    const Cand& cd = cands[c];
+  for (int c = 0; c < kTileKinds; c++) {
+    const TileCost& cd = kTileCosts[c];
     const int64_t tiles = ((M + cd.bm - 1) / cd.bm) * ((N + cd.bn - 1) / cd.bn);
     const int64_t slots = (int64_t)cus * cd.per_cu;
     for (int sp = 1; sp <= 16; sp++) {
       if (sp > 1 && (stages / sp < 4 || tiles * (sp - 1) >= slots)) break;
       const int64_t items = tiles * sp, full = items / slots, rest = (items % slots + cus - 1) / cus;
       const double per = (double)((stages + sp - 1) / sp);
-      double t = kRoundUs[c] + full * per * cd.us[cd.per_cu - 1] + (rest ? per * cd.us[rest - 1] : 0.0);
+      double t = cd.round_us + full * per * cd.us[cd.per_cu - 1] + (rest ? per * cd.us[rest - 1] : 0.0);
       if (sp > 1) t += kSplitUs + 2.0 * sp * M * N * 4 / kPartBytesUs;
       if (t < best_t * 0.999) {
         best_t = t;
-        best = TilePlan{cd.bm, cd.bn, sp};
+        best = TilePlan{(TileKind)c, sp};
       }
     }
   }
@@ -625,16 +659,21 @@ inline size_t tile_workspace(const TilePlan& pl, int64_t M, int64_t N) {
 template <bool kInt8, bool kTransA, bool kTransB, int EPI>
 hipError_t launch_tile(TileArgs a, const TilePlan& pl, hipStream_t stream) {
   const int64_t brows = EPI == kTileGated ? 2 * (int64_t)a.N : a.N;
-  a.tiles_m = (int)((a.M + pl.bm - 1) / pl.bm);
-  a.tiles_n = (int)((brows + pl.bn - 1) / pl.bn);
+  const TileCost& shape = kTileCosts[pl.kind];
+  a.tiles_m = (int)((a.M + shape.bm - 1) / shape.bm);
+  a.tiles_n = (int)((brows + shape.bn - 1) / shape.bn);
   a.splits = pl.splits;
   const unsigned grid = (unsigned)((int64_t)a.tiles_m * a.tiles_n * a.splits);
-  if (pl.bm == 256)
-    tile_gemm<kInt8, 256, 256, 2, 4, kTransA, kTransB, EPI><<<grid, 512, 0, stream>>>(a);
-  else if (pl.bm == 128)
-    tile_gemm<kInt8, 128, 128, 2, 2, kTransA, kTransB, EPI><<<grid, 256, 0, stream>>>(a);
-  else
-    tile_gemm<kInt8, 64, 128, 2, 2, kTransA, kTransB, EPI><<<grid, 256, 0, stream>>>(a);
+#define BSFP4_TILE(BM, BN, WGM, WGN, RING) \
+  tile_gemm<kInt8, BM, BN, WGM, WGN, RING, kTransA, kTransB, EPI><<<grid, 64 * WGM * WGN, 0, stream>>>(a)
+  switch (pl.kind) {
+    case kTile256: BSFP4_TILE(256, 256, 2, 4, 2); break;
+    case kTile128: BSFP4_TILE(128, 128, 2, 2, 2); break;
+    case kTile128Deep: BSFP4_TILE(128, 128, 2, 2, 4); break;
+    case kTile64x128: BSFP4_TILE(64, 128, 2, 2, 3); break;
+    default: BSFP4_TILE(64, 64, 2, 1, 4); break;
+  }
+#undef BSFP4_TILE
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   const int64_t items = (int64_t)a.M * (a.N / 8);
