@@ -27,29 +27,12 @@ constexpr int kRowsStep = 128;             // bytes of K per wave and step: two 
 constexpr int kRowsUnroll = 4;             // steps loaded before any is multiplied
 constexpr int kRowsQuantBytes = 64 * 1024;  // quantised activations kept in LDS
 
-template <bool kInt8>
-struct Mma16;
-template <>
-struct Mma16<false> {
-  typedef v4f Acc;
-  __device__ static __forceinline__ Acc run(v4i a, v4i b, Acc c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
-  }
-};
-template <>
-struct Mma16<true> {
-  typedef v4i Acc;
-  __device__ static __forceinline__ Acc run(v4i a, v4i b, Acc c) {
-    return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
-  }
-};
-
 // MB blocks of 16 activation rows, NB blocks of 16 weight rows (gated: NB = 2, gate
 // and up), WAVES waves.  p as for tile_gemm (operands along K), splits unused.
 template <bool kInt8, int EPI, int MB, int NB, int WAVES, bool kQuant>
 __global__ void __launch_bounds__(64 * WAVES, WAVES / 4)
     rows_gemm(const TileArgs p, const uint16_t* __restrict__ x) {
-  typedef Mma16<kInt8> MM;
+  typedef Mma<kInt8> MM;
   constexpr bool kGated = EPI == kTileGated;
   static_assert(!kGated || NB == 2, "gate and up blocks");
   static_assert(!kQuant || (kInt8 && MB == 1 && !kGated), "fused quantiser");

@@ -4,9 +4,12 @@
 //   acc[m, n] = sum_k A(m, k) B(n, k)
 //
 // bf16 and int8 are the same kernel: a 16-byte chunk is 8 bf16 or 16 int8
-// values, v_mfma_f32_32x32x16_bf16 and v_mfma_i32_32x32x32_i8 each take one such
-// chunk per lane and operand, and both run 32 cycles, so everything is laid out
-// in bytes and only the instruction differs.
+// values, v_mfma_f32_16x16x32_bf16 and v_mfma_i32_16x16x64_i8 each take one such
+// chunk per lane and operand, and both run 16 cycles, so everything is laid out
+// in bytes and only the instruction differs.  The part is power-limited under
+// these products and the 16 x 16 forms take less power per operation than 32 x 32:
+// from registers, on random operands, 1.95 PFLOP/s bf16 and 3.86 POP/s int8
+// against 1.65 and 3.33 (measured).
 //
 // Each operand is stored either with its rows along K (a row of A is one m, K
 // contiguous) or, for bf16, transposed (a row is one k): the backward pass reads
@@ -19,11 +22,11 @@
 // the loads of the RING - 1 stages that follow in flight while a stage is multiplied.
 // LDS layout of a stage, A first:
 //   rows along K   [rows][8 chunks of 16 B], chunk c of row r at position
-//                  c ^ ((r ^ r / 8) & 7): the 32 rows of a fragment read hit
+//                  c ^ tile_swz(r): the 16 rows of a fragment read hit
 //                  distinct bank groups
-//   transposed     [64 k][BM or BN values] in 32-byte units, their pairs
-//                  exchanged by row (tile_tswz): the four k rows of a
-//                  transposing read hit distinct banks
+//   transposed     [64 k][BM or BN values] in 32-byte units, exchanged by row
+//                  (tile_tswz): the k rows of a transposing read hit distinct
+//                  banks
 // Both swizzles are applied to the global address of each lane's 16 bytes, as the
 // LDS side of a direct load is always consecutive.
 //
@@ -46,22 +49,22 @@ namespace {
 constexpr int kTileStage = 128;  // bytes of K per row and stage (rows along K)
 constexpr int kTileStageK = 64;  // k rows per stage (transposed bf16)
 
-typedef int v16i __attribute__((ext_vector_type(16)));
-
 template <bool kInt8>
 struct Mma;
 template <>
 struct Mma<false> {
-  typedef v16f Acc;
+  typedef v4f Acc;
+  typedef float Elem;
   __device__ static __forceinline__ Acc run(v4i a, v4i b, Acc c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
   }
 };
 template <>
 struct Mma<true> {
-  typedef v16i Acc;
+  typedef v4i Acc;
+  typedef int Elem;
   __device__ static __forceinline__ Acc run(v4i a, v4i b, Acc c) {
-    return __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
   }
 };
 
@@ -103,18 +106,21 @@ __device__ __forceinline__ void act_value_grad(int act, float g, float& a, float
 
 // ---- one operand of a tile -------------------------------------------------
 // Position of 16-byte chunk c of row r inside its 128 bytes is c ^ tile_swz(r).
-__device__ __forceinline__ constexpr int tile_swz(int r) { return (r ^ ((r >> 3) & 3)) & 7; }
+__device__ __forceinline__ constexpr int tile_swz(int r) { return (r ^ ((r >> 3) & 1)) & 7; }
 
-// Transposed: pair of 32-byte units u / 2 of k row k is kept at (u / 2) ^
-// tile_tswz.  k rows of 256 bytes or more start at the same bank, those of 128
-// bytes (ROWS 64) alternate between two halves.
+// Transposed: 32-byte unit u (16 values) of k row k is kept at u ^ tile_tswz(k).  A
+// transposing read takes, for each 16 lanes, one unit of four consecutive k rows;
+// 32 lanes read the rows k .. k + 3 and k + 8 .. k + 11.  Rows of 256 bytes or more
+// start at the same bank, those of 128 bytes (ROWS 64) alternate between two halves.
 template <int ROWS>
-__device__ __forceinline__ constexpr int tile_tswz(int k) { return ROWS == 64 ? (k >> 1) & 1 : k & 3; }
+__device__ __forceinline__ constexpr int tile_tswz(int k) {
+  return 2 * (ROWS == 64 ? (k >> 1) & 1 : k & 3) + ((k >> 3) & 1);
+}
 
 // ROWS tile rows (m or n) of one operand, its 1 KB loads shared by WAVES waves
 // (load q = wave * kLoads + j).
 //   rows along K: load q holds tile rows 8q .. 8q + 7; lane l brings position
-//     l % 8 of row 8q + l / 8.  With kPairs the tile rows are blocks of 32
+//     l % 8 of row 8q + l / 8.  With kPairs the tile rows are blocks of 16
 //     alternating between two row ranges (gate and up), each its own buffer.
 //   transposed: load q holds 512 / ROWS k rows.
 template <int ROWS, bool kTrans, bool kPairs, int WAVES>
@@ -146,7 +152,7 @@ struct TileLoader {
       for (int j = 0; j < kLoads; j++) {
         const int k = (q0 + j) * (64 / kLanesRow) + lane / kLanesRow;
         const int pos = lane % kLanesRow;
-        const int col = (((pos >> 1) ^ (2 * tile_tswz<ROWS>(k))) * 16) + (pos & 1) * 8;
+        const int col = ((pos >> 1) ^ tile_tswz<ROWS>(k)) * 16 + (pos & 1) * 8;
         off[j] = first + col < rows ? (uint32_t)(k * ld + col * 2) : kBufOOB;
       }
     } else {
@@ -156,7 +162,7 @@ struct TileLoader {
 #pragma unroll
       for (int j = 0; j < kLoads; j++) {
         const int q = q0 + j, r = 8 * q + lane / 8;
-        const int row = kPairs ? (q >> 3) * 32 + (r & 31) : r;
+        const int row = kPairs ? (q >> 2) * 16 + (r & 15) : r;
         c16[j] = (uint32_t)((lane & 7) ^ tile_swz(r)) * 16;
         off[j] = row < lim ? (uint32_t)(row * ld) + c16[j] : kBufOOB;
       }
@@ -179,41 +185,43 @@ struct TileLoader {
 
   // Load j of stage `st` into LDS at `lds`.
   __device__ __forceinline__ void issue(int j, int st, v4u32 r, uint32_t lds) const {
-    if (kPairs && (((q0 + j) >> 2) & 1)) r = rsrc[kPairs ? 1 : 0];
+    if (kPairs && (((q0 + j) >> 1) & 1)) r = rsrc[kPairs ? 1 : 0];
     buf_lds16(r, off[j], kTrans ? 0u : (uint32_t)st * kTileStage, lds + (uint32_t)(q0 + j) * 1024);
   }
 };
 
-// Fragments of 32-row blocks from a stage in LDS: 16 bytes per lane, K chunk
-// 2 kk + lane / 32 of row lane % 32.
-template <int ROWS, bool kTrans, int T>
+// Fragments of 16-row blocks from a stage in LDS: 16 bytes per lane, K chunk
+// 4 kk + lane / 16 of row lane % 16 (kk 0, 1).
+template <int ROWS, bool kTrans>
 struct TileReader {
-  uint32_t off[kTrans ? T : 4];  // LDS byte offsets inside the operand's stage
+  // LDS byte offsets inside the operand's stage.  transposed: of blocks 0 .. 7 of
+  // the wave's range (whose first block is a multiple of 8, or the range is short)
+  static constexpr int kBlocks = 8;
+  uint32_t off[kTrans ? kBlocks : 2];
   __device__ __forceinline__ void init(int block0, int lane) {
+    const int lr = lane & 15, kg = lane >> 4;
     if constexpr (kTrans) {
-      const int s = (lane & 15) >> 2;
+      const int k = 8 * kg + (lr >> 2);
 #pragma unroll
-      for (int i = 0; i < T; i++)
-        off[i] = (uint32_t)((8 * (lane >> 5) + s) * ROWS * 2 + (2 * ((block0 + i) ^ tile_tswz<ROWS>(s)) + ((lane >> 4) & 1)) * 32 +
-                            (lane & 3) * 8);
+      for (int i = 0; i < kBlocks; i++)
+        off[i] = (uint32_t)(k * ROWS * 2 + ((block0 + i) ^ tile_tswz<ROWS>(k)) * 32 + (lr & 3) * 8);
     } else {
-      const int lr = lane & 31;
 #pragma unroll
-      for (int kk = 0; kk < 4; kk++)
-        off[kk] = (uint32_t)((block0 * 32 + lr) * kTileStage + (((2 * kk + (lane >> 5)) ^ tile_swz(lr)) * 16));
+      for (int kk = 0; kk < 2; kk++)
+        off[kk] = (uint32_t)((block0 * 16 + lr) * kTileStage + (((4 * kk + kg) ^ tile_swz(lr)) * 16));
     }
   }
   __device__ __forceinline__ v4i read(const uint8_t* stage, int i, int kk) const {
     if constexpr (kTrans) {
       typedef short v4s __attribute__((ext_vector_type(4)));
       typedef __attribute__((address_space(3))) v4s lds_v4s;
-      lds_v4s* p = (lds_v4s*)(const __attribute__((address_space(3))) uint8_t*)(stage + off[i] + kk * 16 * ROWS * 2);
+      lds_v4s* p = (lds_v4s*)(const __attribute__((address_space(3))) uint8_t*)(stage + off[i] + kk * 32 * ROWS * 2);
       const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(p);
       const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(p + ROWS);  // four k rows on (8 bytes per element)
       const uint2 a = __builtin_bit_cast(uint2, lo), b = __builtin_bit_cast(uint2, hi);
       return v4i{(int)a.x, (int)a.y, (int)b.x, (int)b.y};
     } else {
-      return *reinterpret_cast<const v4i*>(stage + off[kk] + i * 32 * kTileStage);
+      return *reinterpret_cast<const v4i*>(stage + off[kk] + i * 16 * kTileStage);
     }
   }
 };
@@ -277,16 +285,16 @@ __global__ void __launch_bounds__(64 * WGM * WGN, (tile_waves_simd<BM, BN, RING,
     tile_gemm(const TileArgs p) {
   typedef Mma<kInt8> MM;
   constexpr int NT = 64 * WGM * WGN, WAVES = WGM * WGN;
-  constexpr int WM = BM / WGM, WN = BN / WGN, TM = WM / 32, TN = WN / 32;
+  constexpr int WM = BM / WGM, WN = BN / WGN, TM = WM / 16, TN = WN / 16;
   constexpr int kStageA = BM * kTileStage, kStage = (BM + BN) * kTileStage;
   constexpr bool kGated = EPI == kTileGated;
   static_assert(RING >= 2 && RING <= 4, "ring depth");
-  static_assert(!kGated || TN % 2 == 0, "a wave holds gate / up block pairs");
+  static_assert(!kGated || TN % 2 == 0, "a wave holds pairs of gate and up blocks");
   static_assert(!kInt8 || (!kTransA && !kTransB), "8-bit operands have their rows along K");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[tile_smem<BM, BN, RING>()];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave / WGN, wn = wave % WGN, g = lane >> 5, lr = lane & 31;
+  const int wm = wave / WGN, wn = wave % WGN, kg = lane >> 4, lr = lane & 15;
   int tile_m, tile_n, split;
   tile_item(p, tile_m, tile_n, split);
   constexpr int kCols = kGated ? BN / 2 : BN;  // output columns of a tile
@@ -305,8 +313,9 @@ __global__ void __launch_bounds__(64 * WGM * WGN, (tile_waves_simd<BM, BN, RING,
   // an operand along K beside a transposed one: K counted in bytes there
   const int64_t kend_a = !kTransA && kTransB ? p.kend * 2 : p.kend;
   const int64_t kend_b = !kTransB && kTransA ? p.kend * 2 : p.kend;
-  TileReader<BM, kTransA, TM> ra;
-  TileReader<BN, kTransB, TN> rb;
+  static_assert(TM <= 8 && TN <= 8, "transposed readers hold eight blocks");
+  TileReader<BM, kTransA> ra;
+  TileReader<BN, kTransB> rb;
   ra.init(wm * TM, lane);
   rb.init(wn * TN, lane);
   const uint32_t lds0 = lds_offset(smem);
@@ -316,19 +325,23 @@ __global__ void __launch_bounds__(64 * WGM * WGN, (tile_waves_simd<BM, BN, RING,
 #pragma unroll
     for (int j = 0; j < TN; j++) acc[i][j] = typename MM::Acc{};
 
-  // A stage is four groups kk of TM x TN MFMAs.  The fragments of the next group
-  // are read, and the loads of the stage after next issued, between a group's
-  // MFMAs.  The one barrier of a stage stands in the middle of group 2, where the
-  // wave has all fragments of the stage in registers: past it every wave's loads
-  // of the next stage have landed and the slot just read is free, so group 3
-  // already reads the next stage and the MFMAs run on across it.
-  constexpr int kMfma = TM * TN, kReads = TM + TN;
+  // A stage is 2 kParts groups of MFMAs: two K halves kk, and in each the wave's
+  // rows of A in kParts parts.  The fragments of the next group are read, and the
+  // loads of the stage RING on issued, between a group's MFMAs.  The one barrier of
+  // a stage stands late in its last group but one, where the wave has all fragments
+  // of the stage in registers: past it every wave's loads of the next stage have
+  // landed and the slot just read is free, so the last group already reads the next
+  // stage and the MFMAs run on across it.
+  constexpr int kParts = TM >= 2 ? 2 : 1, TP = TM / kParts, kGroups = 2 * kParts;
+  constexpr int kMfma = TP * TN, kReads = TP + TN;
   constexpr int kIssues = decltype(la)::kLoads + decltype(lb)::kLoads;
-  v4i fa[2][TM], fb[2][TN];
-  auto read_one = [&](int r, int slot, int kk, int buf) {  // fragment r of group kk: B's, then A's
+  v4i fa[2][TP], fb[2][TN];
+  // fragment r of group `grp`: its A rows, then, with a new kk, B's
+  auto read_one = [&](int r, int slot, int grp) {
     const uint8_t* q = smem + slot * kStage;
-    if (r < TN) fb[buf][r] = rb.read(q + kStageA, r, kk);
-    else fa[buf][r - TN] = ra.read(q, r - TN, kk);
+    const int kk = grp / kParts, part = grp % kParts;
+    if (r < TP) fa[grp & 1][r] = ra.read(q, part * TP + r, kk);
+    else if (part == 0) fb[kk & 1][r - TP] = rb.read(q + kStageA, r - TP, kk);
   };
   v4u32 rsa, rsb;
   auto begin_issue = [&](int st) {  // before the loads of stage st
@@ -352,24 +365,26 @@ __global__ void __launch_bounds__(64 * WGM * WGN, (tile_waves_simd<BM, BN, RING,
     asm volatile("" ::: "memory");
   };
   // kLeft: stages that follow (RING: that many or more, so stage st + RING is issued)
-  auto group = [&](auto left_c, int kk, int st, int slot) {
+  auto group = [&](auto left_c, int grp, int st, int slot) {
     constexpr int kLeft = decltype(left_c)::value;
     constexpr bool kNext = kLeft > 0, kAfter = kLeft >= RING;
-    if (kAfter && kk == 3) begin_issue(st + RING);
+    const int kk = grp / kParts, part = grp % kParts;
+    const bool last = grp == kGroups - 1;
+    if (kAfter && last) begin_issue(st + RING);
 #pragma unroll
     for (int t = 0; t < kMfma; t++) {
       const int i = t / TN, j = t % TN;
-      // the B fragment as first operand: a lane ends with four consecutive
-      // columns of one row in each register quad
-      acc[i][j] = MM::run(fb[kk & 1][j], fa[kk & 1][i], acc[i][j]);
-      if (kk < 3 || kNext) {
+      // the B fragment as first operand: a lane ends with four consecutive columns
+      // of one row in its four registers
+      acc[part * TP + i][j] = MM::run(fb[kk & 1][j], fa[grp & 1][i], acc[part * TP + i][j]);
+      if (!last || kNext) {
 #pragma unroll
         for (int r = 0; r < kReads; r++)
-          if (r * (kMfma / 4) / kReads == t) read_one(r, kk < 3 ? slot : slot + 1 == RING ? 0 : slot + 1, (kk + 1) & 3, (kk + 1) & 1);
+          if (r * (kMfma / 2) / kReads == t) read_one(r, !last ? slot : slot + 1 == RING ? 0 : slot + 1, (grp + 1) % kGroups);
       }
-      if (kNext && kk == 2 && t == (kMfma > 1 ? kMfma * 3 / 4 - 1 : 0))
+      if (kNext && grp == kGroups - 2 && t == (kMfma > 1 ? kMfma * 3 / 4 - 1 : 0))
         arrive(std::integral_constant<int, kLeft < RING ? kLeft - 1 : RING - 2>{});
-      if (kAfter && kk == 3) {
+      if (kAfter && last) {
 #pragma unroll
         for (int l = 0; l < kIssues; l++)
           if (l * kMfma / kIssues == t) issue_one(l, st + RING, slot);
@@ -378,10 +393,8 @@ __global__ void __launch_bounds__(64 * WGM * WGN, (tile_waves_simd<BM, BN, RING,
     }
   };
   auto stage = [&](auto left_c, int st, int slot) {
-    group(left_c, 0, st, slot);
-    group(left_c, 1, st, slot);
-    group(left_c, 2, st, slot);
-    group(left_c, 3, st, slot);
+#pragma unroll
+    for (int grp = 0; grp < kGroups; grp++) group(left_c, grp, st, slot);
   };
   const int nst = s1 - s0;
   if (nst > 0) {
@@ -396,7 +409,7 @@ __global__ void __launch_bounds__(64 * WGM * WGN, (tile_waves_simd<BM, BN, RING,
     if (nst >= RING) arrive(std::integral_constant<int, RING - 1>{});
     else arrive(std::integral_constant<int, 0>{});
 #pragma unroll
-    for (int r = 0; r < kReads; r++) read_one(r, 0, 0, 0);
+    for (int r = 0; r < kReads; r++) read_one(r, 0, 0);
     int st = s0, slot = 0;
     auto advance = [&] {
       st++;
@@ -422,26 +435,23 @@ __global__ void __launch_bounds__(64 * WGM * WGN, (tile_waves_simd<BM, BN, RING,
     stage(std::integral_constant<int, 0>{}, st, slot);
   }
 
-  // register 4q + e of block (i, j): row wm*WM + 32 i + lr, tile column wn*WN + 32 j + 8q + 4g + e
+  // register e of block (i, j): row wm WM + 16 i + lr, tile column wn WN + 16 j + 4 kg + e;
+  // gated: even j gate, odd j up, output column wn WN / 2 + 16 (j / 2) + 4 kg + e
+  auto out_col = [&](int j) { return (kGated ? wn * (WN / 2) + (j / 2) * 16 : wn * WN + j * 16) + 4 * kg; };
   if (p.splits > 1) {
     const int64_t width = kGated ? 2 * (int64_t)p.N : p.N;
     float* dst = reinterpret_cast<float*>(p.part) + (int64_t)split * p.M * width;
 #pragma unroll
     for (int i = 0; i < TM; i++) {
-      const int m = m0 + wm * WM + i * 32 + lr;
+      const int m = m0 + wm * WM + i * 16 + lr;
       if (m >= p.M) continue;
 #pragma unroll
-      for (int j = 0; j < TN; j++)
-#pragma unroll
-        for (int q = 0; q < 4; q++) {
-          const int n = n0 + (kGated ? wn * (WN / 2) + (j / 2) * 32 : wn * WN + j * 32) + 8 * q + 4 * g;
-          if (n >= p.N) continue;
-          typedef typename std::conditional<kInt8, int, float>::type T;
-          const T v[4] = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+      for (int j = 0; j < TN; j++) {
+        const int n = n0 + out_col(j);
+        if (n < p.N)
           *reinterpret_cast<uint4*>(dst + (int64_t)m * width + (kGated && (j & 1) ? p.N : 0) + n) =
-              make_uint4(__builtin_bit_cast(uint32_t, v[0]), __builtin_bit_cast(uint32_t, v[1]),
-                         __builtin_bit_cast(uint32_t, v[2]), __builtin_bit_cast(uint32_t, v[3]));
-        }
+              __builtin_bit_cast(uint4, acc[i][j]);
+      }
     }
     return;
   }
@@ -463,58 +473,55 @@ __global__ void __launch_bounds__(64 * WGM * WGN, (tile_waves_simd<BM, BN, RING,
   float sa[TM];
 #pragma unroll
   for (int i = 0; i < TM; i++) {
-    const int m = m0 + wm * WM + i * 32 + lr;
+    const int m = m0 + wm * WM + i * 16 + lr;
     sa[i] = kInt8 && m < p.M ? p.sa[m] : 0.0f;
   }
-  auto quad = [&](int i, int j, int q, const float4& sb) -> float4 {
+  auto quad = [&](int i, int j, const float4& sb) -> float4 {
     const auto& a = acc[i][j];
     if constexpr (kInt8)
-      return make_float4((float)a[4 * q] * sa[i] * sb.x, (float)a[4 * q + 1] * sa[i] * sb.y,
-                         (float)a[4 * q + 2] * sa[i] * sb.z, (float)a[4 * q + 3] * sa[i] * sb.w);
+      return make_float4((float)a[0] * sa[i] * sb.x, (float)a[1] * sa[i] * sb.y, (float)a[2] * sa[i] * sb.z,
+                         (float)a[3] * sa[i] * sb.w);
     else
-      return make_float4(a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]);
+      return make_float4(a[0], a[1], a[2], a[3]);
   };
   auto scales = [&](int n) -> float4 {  // of B rows n .. n + 3
     if constexpr (kInt8) return *reinterpret_cast<const float4*>(p.sb + n);
     else return make_float4(1.0f, 1.0f, 1.0f, 1.0f);
   };
+  auto put4 = [&](int i, int c, const float4& v) {
+    *reinterpret_cast<uint2*>(smem + (wm * WM + i * 16 + lr) * kPitch + c * 2) =
+        make_uint2(pack_bf16x2_ieee(v.x, v.y), pack_bf16x2_ieee(v.z, v.w));
+  };
   if constexpr (!kGated) {
 #pragma unroll
-    for (int j = 0; j < TN; j++)
-#pragma unroll
-      for (int q = 0; q < 4; q++) {
-        const int c = wn * WN + j * 32 + 8 * q + 4 * g, n = min(n0 + c, p.N - 4);
-        const float4 sb = scales(n);
-        float4 bv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (kInt8 && p.bias) {
-          const uint2 b = *reinterpret_cast<const uint2*>(p.bias + n);
-          bv = make_float4(bf16_lo(b.x), bf16_hi(b.x), bf16_lo(b.y), bf16_hi(b.y));
-        }
-#pragma unroll
-        for (int i = 0; i < TM; i++) {
-          float4 v = quad(i, j, q, sb);
-          if (kInt8) v = make_float4(v.x + bv.x, v.y + bv.y, v.z + bv.z, v.w + bv.w);
-          *reinterpret_cast<uint2*>(smem + (wm * WM + i * 32 + lr) * kPitch + c * 2) =
-              make_uint2(pack_bf16x2_ieee(v.x, v.y), pack_bf16x2_ieee(v.z, v.w));
-        }
+    for (int j = 0; j < TN; j++) {
+      const int c = out_col(j), n = min(n0 + c, p.N - 4);
+      const float4 sb = scales(n);
+      float4 bv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (kInt8 && p.bias) {
+        const uint2 b = *reinterpret_cast<const uint2*>(p.bias + n);
+        bv = make_float4(bf16_lo(b.x), bf16_hi(b.x), bf16_lo(b.y), bf16_hi(b.y));
       }
+#pragma unroll
+      for (int i = 0; i < TM; i++) {
+        float4 v = quad(i, j, sb);
+        if (kInt8) v = make_float4(v.x + bv.x, v.y + bv.y, v.z + bv.z, v.w + bv.w);
+        put4(i, c, v);
+      }
+    }
     flush(p.D, p.N);
   } else {
 #pragma unroll
-    for (int j = 0; j < TN; j += 2)
+    for (int j = 0; j < TN; j += 2) {
+      const int c = out_col(j), n = min(n0 + c, p.N - 4);
+      const float4 sg = scales(n), su = scales(p.N + n);
 #pragma unroll
-      for (int q = 0; q < 4; q++) {
-        const int c = wn * (WN / 2) + (j / 2) * 32 + 8 * q + 4 * g, n = min(n0 + c, p.N - 4);
-        const float4 sg = scales(n), su = scales(p.N + n);
-#pragma unroll
-        for (int i = 0; i < TM; i++) {
-          const float4 gv = quad(i, j, q, sg), uv = quad(i, j + 1, q, su);
-          const int r = wm * WM + i * 32 + lr;
-          *reinterpret_cast<uint2*>(smem + r * kPitch + c * 2) =
-              make_uint2(pack_bf16x2_ieee(act_value(p.act, gv.x) * uv.x, act_value(p.act, gv.y) * uv.y),
-                         pack_bf16x2_ieee(act_value(p.act, gv.z) * uv.z, act_value(p.act, gv.w) * uv.w));
-        }
+      for (int i = 0; i < TM; i++) {
+        const float4 gv = quad(i, j, sg), uv = quad(i, j + 1, su);
+        put4(i, c, make_float4(act_value(p.act, gv.x) * uv.x, act_value(p.act, gv.y) * uv.y,
+                               act_value(p.act, gv.z) * uv.z, act_value(p.act, gv.w) * uv.w));
       }
+    }
     flush(p.D, p.N);
     if constexpr (!kInt8) {
       if (p.gate_up) {  // the sums as they are, gate then up, in whole row segments as well
@@ -526,13 +533,8 @@ __global__ void __launch_bounds__(64 * WGM * WGN, (tile_waves_simd<BM, BN, RING,
 #pragma unroll
           for (int j = half; j < TN; j += 2)
 #pragma unroll
-            for (int q = 0; q < 4; q++) {
-              const int c = wn * (WN / 2) + (j / 2) * 32 + 8 * q + 4 * g;
-#pragma unroll
-              for (int i = 0; i < TM; i++)
-                *reinterpret_cast<float4*>(smem + (wm * WM + i * 32 + lr) * kPitch4 + c * 4) =
-                    make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
-            }
+            for (int i = 0; i < TM; i++)
+              *reinterpret_cast<v4f*>(smem + (wm * WM + i * 16 + lr) * kPitch4 + out_col(j) * 4) = acc[i][j];
           __syncthreads();
           constexpr int kChunksRow = kCols / 4;
           for (int idx = tid; idx < BM * kChunksRow; idx += NT) {
@@ -553,7 +555,7 @@ __global__ void __launch_bounds__(64 * WGM * WGN, (tile_waves_simd<BM, BN, RING,
 template <bool kInt8, int EPI>
 __global__ void __launch_bounds__(256)
     tile_reduce(const TileArgs p) {
-  typedef typename std::conditional<kInt8, int, float>::type T;
+  typedef typename Mma<kInt8>::Elem T;
   constexpr bool kGated = EPI == kTileGated;
   const int64_t width = kGated ? 2 * (int64_t)p.N : p.N;
   const int64_t mn = (int64_t)p.M * width;
@@ -671,7 +673,7 @@ hipError_t launch_tile(TileArgs a, const TilePlan& pl, hipStream_t stream) {
     case kTile128: BSFP4_TILE(128, 128, 2, 2, 2); break;
     case kTile128Deep: BSFP4_TILE(128, 128, 2, 2, 4); break;
     case kTile64x128: BSFP4_TILE(64, 128, 2, 2, 3); break;
-    default: BSFP4_TILE(64, 64, 2, 1, 4); break;
+    default: BSFP4_TILE(64, 64, 2, 2, 4); break;
   }
 #undef BSFP4_TILE
   hipError_t e = hipGetLastError();
