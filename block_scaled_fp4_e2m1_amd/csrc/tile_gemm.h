@@ -243,6 +243,7 @@ struct TileArgs {
   uint16_t* D;         // [M, N]
   float* gate_up;      // gated: the sums [M, 2 N] or null
   int act;
+  int m_base, n_base;  // first row and column of this launch
   int tiles_m, tiles_n, splits;
   void* part;          // splits > 1: float / int32 [splits][M][N or 2 N]
 };
@@ -254,11 +255,15 @@ constexpr int tile_smem() {
   return ring > out ? ring : out;
 }
 
-// Waves per SIMD that the LDS lets in: what the registers are sized for.
+// Waves per SIMD that the LDS lets in: what the registers are sized for.  Every
+// kernel has two at least: with the 512 registers of a single one the compiler keeps
+// accumulators in the second bank and copies them around (measured 24 % slower, int8
+// 128 x 128 with four slots on four waves against eight).
 template <int BM, int BN, int RING, int WAVES>
 constexpr int tile_waves_simd() {
-  const int w = 160 * 1024 / tile_smem<BM, BN, RING>() * WAVES / 4;
-  return w < 1 ? 1 : w;
+  constexpr int w = 160 * 1024 / tile_smem<BM, BN, RING>() * WAVES / 4;
+  static_assert(w >= 2, "two waves per SIMD");
+  return w;
 }
 
 // Work item of a workgroup.  Workgroups are dispatched round-robin over the 8
@@ -298,7 +303,7 @@ __global__ void __launch_bounds__(64 * WGM * WGN, (tile_waves_simd<BM, BN, RING,
   int tile_m, tile_n, split;
   tile_item(p, tile_m, tile_n, split);
   constexpr int kCols = kGated ? BN / 2 : BN;  // output columns of a tile
-  const int m0 = tile_m * BM, n0 = tile_n * kCols;
+  const int m0 = p.m_base + tile_m * BM, n0 = p.n_base + tile_n * kCols;
 
   constexpr int64_t kStep = (kTransA || kTransB) ? kTileStageK : kTileStage;
   const int total = (int)((p.kend + kStep - 1) / kStep);
@@ -606,48 +611,74 @@ __global__ void __launch_bounds__(256)
 // The kernels of a product.  A large tile does the most with each byte in LDS; a
 // small one with more slots has more loads under way per multiplied stage, which is
 // what a product of few workgroups waits for.
-enum TileKind { kTile256, kTile128, kTile128Deep, kTile64x128, kTile64, kTileKinds };
+enum TileKind { kTile256, kTile256x128, kTile128, kTile128Deep, kTile64x128, kTile64, kTileKinds };
 
 struct TilePlan {
   TileKind kind;
   int splits;
+  // Whole rounds of workgroups only: the output rows (or columns, of weight rows)
+  // from `cut` on are a second launch of kernel `rest`.  0: everything in one.
+  int64_t cut_m, cut_n;
+  TileKind rest;
 };
 
-// Kernel and K split of an M x N (x K bytes) product: the pair with the least
+// Kernel and K split of an M x N (x K bytes) product: the choice with the least
 // estimated time.  A stage takes a workgroup us[c - 1] microseconds when c share a
 // compute unit, its start and end round_us; a split's second kernel costs kSplitUs
 // and its partials their bytes.  The figures are a least-squares fit to 2034 timed
 // (shape, kernel, split) combinations, M 48 .. 4096, weights of 1536 x 2048 .. 14336 x
-// 4096, bf16 and int8 (9 % rms); the plan's choice is 0.8 % slower than the best of
-// each shape on average, 11 % at worst.  N counts weight rows (gated: both halves).
+// 4096, bf16 and int8 (9 % rms); the plan's choice is 0.9 % slower than the best of
+// each shape on average, 12 % at worst.  N counts weight rows (gated: both halves).
 struct TileCost {
   int bm, bn, per_cu;
   double us[2], round_us;
 };
-constexpr TileCost kTileCosts[kTileKinds] = {{256, 256, 1, {1.06, 0}, 5.3},
-                                             {128, 128, 2, {0.59, 0.83}, 2.6},
-                                             {128, 128, 1, {0.50, 0}, 3.2},
-                                             {64, 128, 2, {0.31, 0.56}, 3.3},
-                                             {64, 64, 2, {0.265, 0.36}, 3.1}};
+constexpr TileCost kTileCosts[kTileKinds] = {{256, 256, 1, {1.10, 0}, 4.7},  {256, 128, 1, {0.677, 0}, 3.6},
+                                             {128, 128, 2, {0.59, 0.786}, 2.4}, {128, 128, 1, {0.474, 0}, 3.2},
+                                             {64, 128, 2, {0.308, 0.547}, 3.1}, {64, 64, 2, {0.226, 0.357}, 2.8}};
+
+// Estimated time of `items` workgroups of `stages` stages each.
+inline double tile_time(const TileCost& c, int64_t items, double stages, int cus) {
+  const int64_t slots = (int64_t)cus * c.per_cu, full = items / slots, rest = (items % slots + cus - 1) / cus;
+  return c.round_us + full * stages * c.us[c.per_cu - 1] + (rest ? stages * c.us[rest - 1] : 0.0);
+}
 
 inline TilePlan plan_tile(int64_t M, int64_t N, int64_t kbytes, int cus) {
-  constexpr double kSplitUs = 3.0, kPartBytesUs = 4.8e6;
+  constexpr double kSplitUs = 3.3, kPartBytesUs = 5.0e6;
   const int64_t stages = (kbytes + kTileStage - 1) / kTileStage;
-  TilePlan best{kTile256, 1};
+  auto tiles = [](const TileCost& c, int64_t m, int64_t n) { return ((m + c.bm - 1) / c.bm) * ((n + c.bn - 1) / c.bn); };
+  TilePlan best{kTile256, 1, 0, 0, kTile256};
   double best_t = 1e300;
+  auto consider = [&](double t, const TilePlan& pl) {
+    if (t < best_t * 0.999) {
+      best_t = t;
+      best = pl;
+    }
+  };
   for (int c = 0; c < kTileKinds; c++) {
     const TileCost& cd = kTileCosts[c];
-    const int64_t tiles = ((M + cd.bm - 1) / cd.bm) * ((N + cd.bn - 1) / cd.bn);
-    const int64_t slots = (int64_t)cus * cd.per_cu;
+    const int64_t all = tiles(cd, M, N), slots = (int64_t)cus * cd.per_cu;
     for (int sp = 1; sp <= 16; sp++) {
-      if (sp > 1 && (stages / sp < 4 || tiles * (sp - 1) >= slots)) break;
-      const int64_t items = tiles * sp, full = items / slots, rest = (items % slots + cus - 1) / cus;
-      const double per = (double)((stages + sp - 1) / sp);
-      double t = cd.round_us + full * per * cd.us[cd.per_cu - 1] + (rest ? per * cd.us[rest - 1] : 0.0);
+      if (sp > 1 && (stages / sp < 4 || all * (sp - 1) >= slots)) break;
+      double t = tile_time(cd, all * sp, (double)((stages + sp - 1) / sp), cus);
       if (sp > 1) t += kSplitUs + 2.0 * sp * M * N * 4 / kPartBytesUs;
-      if (t < best_t * 0.999) {
-        best_t = t;
-        best = TilePlan{(TileKind)c, sp};
+      consider(t, TilePlan{(TileKind)c, sp, 0, 0, kTile256});
+    }
+    // a part-filled last round (896 tiles of 256 x 256 on 256 units: 3.5 rounds) goes
+    // to smaller tiles: measured at 4096 x 14336 x 4096, gated, 365 -> 340 us
+    const int64_t full = all / slots * slots;
+    if (c > kTile128 || full == 0 || full == all) continue;
+    const int64_t tm = (M + cd.bm - 1) / cd.bm, tn = (N + cd.bn - 1) / cd.bn;
+    for (int dir = 0; dir < 2; dir++) {
+      const int64_t lines = full / (dir ? tm : tn);  // whole tile rows (0) or columns (1) of the main part
+      if (lines == 0) continue;
+      const int64_t cut = lines * (dir ? cd.bn : cd.bm);
+      const double t_main = tile_time(cd, lines * (dir ? tm : tn), (double)stages, cus);
+      for (int r = 0; r < kTileKinds; r++) {
+        const TileCost& rd = kTileCosts[r];
+        const int64_t left = dir ? tiles(rd, M, N - cut) : tiles(rd, M - cut, N);
+        consider(t_main + tile_time(rd, left, (double)stages, cus),
+                 TilePlan{(TileKind)c, 1, dir ? 0 : cut, dir ? cut : 0, (TileKind)r});
       }
     }
   }
@@ -659,24 +690,39 @@ inline size_t tile_workspace(const TilePlan& pl, int64_t M, int64_t N) {
 }
 
 template <bool kInt8, bool kTransA, bool kTransB, int EPI>
-hipError_t launch_tile(TileArgs a, const TilePlan& pl, hipStream_t stream) {
-  const int64_t brows = EPI == kTileGated ? 2 * (int64_t)a.N : a.N;
-  const TileCost& shape = kTileCosts[pl.kind];
-  a.tiles_m = (int)((a.M + shape.bm - 1) / shape.bm);
-  a.tiles_n = (int)((brows + shape.bn - 1) / shape.bn);
-  a.splits = pl.splits;
+hipError_t launch_tile_part(const TileArgs& a, TileKind kind, hipStream_t stream) {
   const unsigned grid = (unsigned)((int64_t)a.tiles_m * a.tiles_n * a.splits);
 #define BSFP4_TILE(BM, BN, WGM, WGN, RING) \
   tile_gemm<kInt8, BM, BN, WGM, WGN, RING, kTransA, kTransB, EPI><<<grid, 64 * WGM * WGN, 0, stream>>>(a)
-  switch (pl.kind) {
+  switch (kind) {
     case kTile256: BSFP4_TILE(256, 256, 2, 4, 2); break;
+    case kTile256x128: BSFP4_TILE(256, 128, 4, 2, 3); break;
     case kTile128: BSFP4_TILE(128, 128, 2, 2, 2); break;
-    case kTile128Deep: BSFP4_TILE(128, 128, 2, 2, 4); break;
+    case kTile128Deep: BSFP4_TILE(128, 128, 2, 4, 4); break;
     case kTile64x128: BSFP4_TILE(64, 128, 2, 2, 3); break;
     default: BSFP4_TILE(64, 64, 2, 2, 4); break;
   }
 #undef BSFP4_TILE
-  hipError_t e = hipGetLastError();
+  return hipGetLastError();
+}
+
+template <bool kInt8, bool kTransA, bool kTransB, int EPI>
+hipError_t launch_tile(TileArgs a, const TilePlan& pl, hipStream_t stream) {
+  constexpr int kHalf = EPI == kTileGated ? 2 : 1;  // weight rows per output column
+  const int64_t brows = kHalf * (int64_t)a.N;
+  auto part = [&](TileKind kind, int64_t m0, int64_t m1, int64_t n0, int64_t n1) {
+    const TileCost& c = kTileCosts[kind];
+    a.m_base = (int)m0;
+    a.n_base = (int)(n0 / kHalf);
+    a.tiles_m = (int)((m1 - m0 + c.bm - 1) / c.bm);
+    a.tiles_n = (int)((n1 - n0 + c.bn - 1) / c.bn);
+    return launch_tile_part<kInt8, kTransA, kTransB, EPI>(a, kind, stream);
+  };
+  a.splits = pl.splits;
+  const int64_t m1 = pl.cut_m ? pl.cut_m : a.M, n1 = pl.cut_n ? pl.cut_n : brows;
+  hipError_t e = part(pl.kind, 0, m1, 0, n1);
+  if (e == hipSuccess && m1 < a.M) e = part(pl.rest, m1, a.M, 0, brows);
+  if (e == hipSuccess && n1 < brows) e = part(pl.rest, 0, a.M, n1, brows);
   if (e != hipSuccess || a.splits == 1) return e;
   const int64_t items = (int64_t)a.M * (a.N / 8);
   tile_reduce<kInt8, EPI><<<(unsigned)std::min<int64_t>((items + 255) / 256, 8192), 256, 0, stream>>>(a);
