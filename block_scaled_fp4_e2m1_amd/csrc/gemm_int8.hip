@@ -9,21 +9,12 @@
 #include "rows_gemm.h"
 
 namespace bsfp4 {
-namespace {
-
-// Rows up to which every workgroup of the product quantises the activations for
-// itself: each reads all of x, so the work grows with M while the launch saved
-// does not.
-constexpr int64_t kFusedQuantRows = 4;
-
-}  // namespace
-
 size_t int8_gemm_workspace(int64_t M, int64_t N, int64_t K) {
   if (rows_ok(M)) return 0;
   return tile_workspace(plan_tile(M, N, K, device_cu_count()), M, N);
 }
 
-bool int8_fused_quant_ok(int64_t M, int64_t K) { return M <= kFusedQuantRows && M * K <= kRowsQuantBytes; }
+bool int8_fused_quant_ok(int64_t M, int64_t K) { return rows_quant_ok(M, K); }
 
 hipError_t launch_int8_fused_quant_gemm(const uint16_t* x, const int8_t* B, const float* sb, const uint16_t* bias,
                                         uint16_t* D, int64_t M, int64_t N, int64_t K, hipStream_t stream) {
@@ -36,7 +27,7 @@ hipError_t launch_int8_fused_quant_gemm(const uint16_t* x, const int8_t* B, cons
   a.sb = sb;
   a.bias = bias;
   a.D = D;
-  return launch_rows_shape<true, kTileStore, 1, 1, true>(a, x, stream);
+  return launch_rows_quant(a, x, stream);
 }
 
 size_t int8_gated_workspace(int64_t M, int64_t I, int64_t K) { return int8_gemm_workspace(M, 2 * I, K); }

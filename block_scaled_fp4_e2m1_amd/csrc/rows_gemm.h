@@ -1,20 +1,23 @@
-// Products of few rows (M <= 32): the weight is read once, straight from memory
-// into the matrix cores' operand registers.
+// Products of few rows (M <= 16), bound by the weight's bytes.
 //
-// Bound by the weight's bytes.  A workgroup owns 16 NB weight rows (gated: 16 gate
-// and 16 up rows) and all M activation rows; its waves take the 128-byte steps of
-// K in turn, so that the workgroup reads whole stretches of its rows and a
-// thousand and more 16-byte loads per compute unit are in flight without any LDS
-// ring or barrier in the loop.  v_mfma_*_16x16x{32, 64} takes the weight as its first
-// operand: lane l supplies 16 bytes of weight row l % 16 and of activation row
-// l % 16, K group l / 16 (the same bytes of both, so any order of K is right), and
-// ends with weight rows 4 (l / 16) .. + 3 of activation row l % 16.  The waves'
-// sums meet in LDS and are added in wave order; one wave per 16 activation rows
-// finishes them.  Activation rows beyond M repeat the last row and are dropped.
+// A workgroup owns 16 weight rows (gated: 8 gate rows and their 8 up rows) and all M
+// activation rows; its eight waves take the 128-byte steps of K in turn.  Each wave
+// runs a ring of its own in LDS, filled by direct loads of eight rows x 128 bytes, so
+// there is no barrier until the waves' sums meet at the end.  The loads go through
+// LDS, though every byte is used by one wave only, because the memory pipeline
+// takes a request per 128-byte line: operands loaded straight into the MFMA's
+// registers (16 rows x 64 bytes per load, twice the lines) ran at 33 GB/s per
+// compute unit against 70 this way (measured; 48 workgroups, bf16 gated 1 x 2048 x 768
+// 6.4 us that way).
 //
-// kQuant (8-bit, M K <= kRowsQuantBytes): the activations come in bf16 and every
-// workgroup quantises all of them into LDS itself, its first weight loads already
-// under way: one launch and no intermediate for a token's projection.
+// v_mfma_*_16x16x{32, 64} takes the weight as its first operand: lane l ends with
+// weight rows 4 (l / 16) .. + 3 of activation row l % 16.  Rows outside the operands
+// and chunks past K are zeros through the buffers' range check.  The waves' sums are
+// added in wave order by one wave, which finishes the outputs.
+//
+// kQuant (8-bit): the activations come in bf16 and every workgroup quantises all of
+// them into LDS itself, its first weight loads already under way: one launch and no
+// intermediate for a token's projection.
 #pragma once
 
 #include "tile_gemm.h"
@@ -22,158 +25,147 @@
 namespace bsfp4 {
 namespace {
 
-constexpr int kRowsMaxM = 32;
-constexpr int kRowsStep = 128;             // bytes of K per wave and step: two MFMAs
-constexpr int kRowsUnroll = 4;             // steps loaded before any is multiplied
-constexpr int kRowsQuantBytes = 64 * 1024;  // quantised activations kept in LDS
+constexpr int kRowsMaxM = 16;
+constexpr int kRowsWaves = 8;
+constexpr int kRowsQuantBytes = 28 * 1024;  // quantised activations kept in LDS
 
-// MB blocks of 16 activation rows, NB blocks of 16 weight rows (gated: NB = 2, gate
-// and up), WAVES waves.  p as for tile_gemm (operands along K), splits unused.
-template <bool kInt8, int EPI, int MB, int NB, int WAVES, bool kQuant>
-__global__ void __launch_bounds__(64 * WAVES, WAVES / 4)
+// Ring slots per wave: two workgroups per compute unit (80 KB each).
+template <int AQ>
+constexpr int rows_ring() { return AQ == 2 ? 2 : 3; }
+template <int AQ>
+constexpr int rows_slot() { return (2 + AQ) * 1024; }
+
+// AQ: 1 KB loads of activations per step (1: M <= 8, 2: M <= 16, 0: kQuant).
+// p as for tile_gemm (operands along K), splits unused.
+template <bool kInt8, int EPI, int AQ>
+__global__ void __launch_bounds__(64 * kRowsWaves, 4)
     rows_gemm(const TileArgs p, const uint16_t* __restrict__ x) {
   typedef Mma<kInt8> MM;
-  constexpr bool kGated = EPI == kTileGated;
-  static_assert(!kGated || NB == 2, "gate and up blocks");
-  static_assert(!kQuant || (kInt8 && MB == 1 && !kGated), "fused quantiser");
-  constexpr int kTiles = MB * NB;
-  extern __shared__ __attribute__((aligned(16))) uint8_t rows_smem[];  // quantised rows, then (reused) the sums
-  __shared__ uint32_t red_max[kQuant ? 4 * WAVES : 1];
-  __shared__ float row_scale[kQuant ? 16 : 1];
+  constexpr bool kGated = EPI == kTileGated, kQuant = AQ == 0;
+  static_assert(!kQuant || (kInt8 && !kGated), "fused quantiser");
+  constexpr int W = kRowsWaves, RING = rows_ring<AQ>(), kSlot = rows_slot<AQ>(), kL = 2 + AQ;
+  constexpr int kRings = W * RING * kSlot;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kRings + (kQuant ? kRowsQuantBytes : 0)];
+  __shared__ int red_max[kQuant ? 4 * W : 1];
+  __shared__ float row_scale[kQuant ? 4 : 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lr = lane & 15, kg = lane >> 4;
-  const int n0 = blockIdx.x * (kGated ? 16 : 16 * NB);
+  const int n0 = blockIdx.x * (kGated ? 8 : 16);
   const int kb = (int)p.kend;
 
-  const uint8_t* w[NB];
+  // weight rows: buffers of the two loads (gated: gate, up), lane offsets inside
+  const int row8 = lane >> 3;  // row of a load
+  const v4u32 rw0 = make_rsrc4(p.B + (int64_t)n0 * p.ldb, (int64_t)min(kGated ? 8 : 16, p.N - n0) * p.ldb);
+  const v4u32 rw1 = kGated ? make_rsrc4(p.B + ((int64_t)p.N + n0) * p.ldb, 8 * p.ldb) : rw0;
+  const v4u32 ra = make_rsrc4(p.A, (int64_t)p.M * p.lda);
+  uint32_t c16[2], ow[2], oa[2];
 #pragma unroll
-  for (int j = 0; j < NB; j++) {
-    // rows past N repeat the last one; their columns are not stored
-    const int64_t row = kGated ? (int64_t)j * p.N + min(n0 + lr, p.N - 1) : min(n0 + 16 * j + lr, p.N - 1);
-    w[j] = p.B + row * p.ldb + kg * 16;
+  for (int q = 0; q < 2; q++) {
+    const int r = 8 * q + row8;
+    c16[q] = (uint32_t)((lane & 7) ^ tile_swz(r)) * 16;
+    ow[q] = (uint32_t)((kGated ? row8 : r) * p.ldb) + c16[q];
+    oa[q] = r < p.M ? (uint32_t)(r * p.lda) + c16[q] : kBufOOB;
   }
-  const uint8_t* a[MB];
+  const uint32_t ring0 = lds_offset(smem) + (uint32_t)wave * RING * kSlot;
+  const uint8_t* const ring = smem + wave * RING * kSlot;
+  auto issue = [&](int s, int slot) {
+    const uint32_t soff = (uint32_t)s * kTileStage, lds = ring0 + (uint32_t)slot * kSlot;
+    const int left = kb - (int)soff;  // a partial last step masks its chunks past K
 #pragma unroll
-  for (int i = 0; i < MB; i++) a[i] = p.A + (int64_t)min(16 * i + lr, p.M - 1) * p.lda + kg * 16;
-
-  typename MM::Acc acc[MB][NB];
+    for (int q = 0; q < 2; q++)
+      buf_lds16(q ? rw1 : rw0, (int)c16[q] < left ? ow[q] : kBufOOB, soff, lds + q * 1024);
 #pragma unroll
-  for (int i = 0; i < MB; i++)
-#pragma unroll
-    for (int j = 0; j < NB; j++) acc[i][j] = typename MM::Acc{};
-
-  const int full = kb / kRowsStep;
-  v4i wr[kRowsUnroll][2][NB];
-  auto load_w = [&](int u, int s) {
-#pragma unroll
-    for (int h = 0; h < 2; h++)
-#pragma unroll
-      for (int j = 0; j < NB; j++)
-        wr[u][h][j] = *reinterpret_cast<const v4i*>(w[j] + (int64_t)s * kRowsStep + h * 64);
+    for (int q = 0; q < AQ; q++) buf_lds16(ra, (int)c16[q] < left ? oa[q] : kBufOOB, soff, lds + (2 + q) * 1024);
   };
-  auto load_a = [&](int i, int s, int h) -> v4i {
-    if constexpr (kQuant)
-      return *reinterpret_cast<const v4i*>(rows_smem + min(lr, p.M - 1) * kb + s * kRowsStep + h * 64 + kg * 16);
-    else
-      return *reinterpret_cast<const v4i*>(a[i] + (int64_t)s * kRowsStep + h * 64);
-  };
+  const int total = (kb + kTileStage - 1) / kTileStage;
+  const int mine = wave < total ? (total - 1 - wave) / W + 1 : 0;  // steps wave, wave + W, ...
+#pragma unroll
+  for (int r = 0; r < RING; r++)
+    if (r < mine) issue(wave + r * W, r);
 
-  int s = wave;
   if constexpr (kQuant) {
-    // the first weight steps are on their way while the rows are quantised
+    // all M <= 4 rows, a chunk of eight values at a time; a row's codes are kept in
+    // whole steps of 128 bytes, its chunks past K zero
+    const int chunks = kb / 8, kept = total * (kTileStage / 8);
+    int mx[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int u = 0; u < kRowsUnroll; u++)
-      if (s + u * WAVES < full) load_w(u, s + u * WAVES);
-    const int chunks = kb / 8;  // 16-byte bf16 chunks of a row
-    for (int m0 = 0; m0 < p.M; m0 += 4) {
-      uint32_t mx[4] = {0, 0, 0, 0};
-      for (int m = 0; m < 4 && m0 + m < p.M; m++) {
-        const uint4* row = reinterpret_cast<const uint4*>(x + (int64_t)(m0 + m) * kb);
-        for (int c = threadIdx.x; c < chunks; c += 64 * WAVES) mx[m] = amax_bits8(row[c], mx[m]);
+    for (int m = 0; m < 4; m++)
+      if (m < p.M)
+        for (int c = threadIdx.x; c < chunks; c += 64 * W)
+          mx[m] = (int)amax_bits8(reinterpret_cast<const uint4*>(x + (int64_t)m * kb)[c], (uint32_t)mx[m]);
+    row_reduce<64 * W>(mx, red_max, MaxOp{});
+#pragma unroll
+    for (int m = 0; m < 4; m++)
+      if (m < p.M) {
+        const Int8Row r((uint32_t)mx[m]);
+        for (int c = threadIdx.x; c < kept; c += 64 * W)
+          *reinterpret_cast<uint2*>(smem + kRings + m * kept * 8 + c * 8) =
+              c < chunks ? r.codes8(reinterpret_cast<const uint4*>(x + (int64_t)m * kb)[c]) : make_uint2(0, 0);
+        if (threadIdx.x == 0) row_scale[m] = r.s;
       }
-#pragma unroll
-      for (int m = 0; m < 4; m++) {
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) mx[m] = max(mx[m], (uint32_t)__shfl_xor((int)mx[m], o, 64));
-        if (lane == 0) red_max[m * WAVES + wave] = mx[m];
-      }
-      __syncthreads();
-      for (int m = 0; m < 4 && m0 + m < p.M; m++) {
-        uint32_t v = red_max[m * WAVES];
-#pragma unroll
-        for (int k = 1; k < WAVES; k++) v = max(v, red_max[m * WAVES + k]);
-        const Int8Row r(v);
-        const uint4* row = reinterpret_cast<const uint4*>(x + (int64_t)(m0 + m) * kb);
-        for (int c = threadIdx.x; c < chunks; c += 64 * WAVES)
-          *reinterpret_cast<uint2*>(rows_smem + (m0 + m) * kb + c * 8) = r.codes8(row[c]);
-        if (threadIdx.x == 0) row_scale[m0 + m] = r.s;
-      }
-      __syncthreads();
-    }
+    // the codes are in LDS; the weight loads stay in flight
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
   }
-  for (bool first = kQuant; s < full; s += kRowsUnroll * WAVES, first = false) {
-    v4i ar[kRowsUnroll][2][MB];
-    if (!first) {
+
+  typename MM::Acc acc{};
+  // lane offsets of the two K halves of a step: row lr, chunk 4 h + kg
+  uint32_t off[2];
 #pragma unroll
-      for (int u = 0; u < kRowsUnroll; u++)
-        if (s + u * WAVES < full) load_w(u, s + u * WAVES);
-    }
-#pragma unroll
-    for (int u = 0; u < kRowsUnroll; u++)
-      if (s + u * WAVES < full)
-#pragma unroll
-        for (int h = 0; h < 2; h++)
-#pragma unroll
-          for (int i = 0; i < MB; i++) ar[u][h][i] = load_a(i, s + u * WAVES, h);
-#pragma unroll
-    for (int u = 0; u < kRowsUnroll; u++)
-      if (s + u * WAVES < full)
-#pragma unroll
-        for (int h = 0; h < 2; h++)
-#pragma unroll
-          for (int i = 0; i < MB; i++)
-#pragma unroll
-            for (int j = 0; j < NB; j++) acc[i][j] = MM::run(wr[u][h][j], ar[u][h][i], acc[i][j]);
-  }
-  // K past the last whole step: the wave whose turn it is, chunk by chunk
-  if (full * kRowsStep < kb && wave == full % WAVES) {
+  for (int h = 0; h < 2; h++) off[h] = (uint32_t)(lr * kTileStage + (((4 * h + kg) ^ tile_swz(lr)) * 16));
+  auto step = [&](int i, int slot) {
+    const uint8_t* s = ring + slot * kSlot;
+    v4i w[2], a[2];
 #pragma unroll
     for (int h = 0; h < 2; h++) {
-      const bool in = full * kRowsStep + h * 64 + kg * 16 < kb;
-      v4i wv[NB], av[MB];
-#pragma unroll
-      for (int j = 0; j < NB; j++)
-        wv[j] = in ? *reinterpret_cast<const v4i*>(w[j] + (int64_t)full * kRowsStep + h * 64) : v4i{0, 0, 0, 0};
-#pragma unroll
-      for (int i = 0; i < MB; i++) {
-        av[i] = v4i{0, 0, 0, 0};
-        if (in) av[i] = load_a(i, full, h);
+      w[h] = *reinterpret_cast<const v4i*>(s + off[h]);
+      if constexpr (kQuant) {
+        const int at = min(lr, p.M - 1) * total * kTileStage + (wave + i * W) * kTileStage + h * 64 + kg * 16;
+        a[h] = *reinterpret_cast<const v4i*>(smem + kRings + at);
+      } else {
+        // M <= 8: the upper eight rows of the fragment repeat the lower (outputs not stored)
+        a[h] = *reinterpret_cast<const v4i*>(s + 2048 + (AQ == 1 ? off[h] & 1023u : off[h]));
       }
+    }
+    // the fragments are in registers before the slot is filled again
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (i + RING < mine) issue(wave + (i + RING) * W, slot);
 #pragma unroll
-      for (int i = 0; i < MB; i++)
-#pragma unroll
-        for (int j = 0; j < NB; j++) acc[i][j] = MM::run(wv[j], av[i], acc[i][j]);
+    for (int h = 0; h < 2; h++) acc = MM::run(w[h], a[h], acc);
+  };
+  int i = 0, slot = 0;
+  for (; i + RING <= mine; i++) {
+    wait_vmcnt<(RING - 1) * kL>();  // the loads of the RING - 1 steps after this one may be under way
+    step(i, slot);
+    slot = slot + 1 == RING ? 0 : slot + 1;
+  }
+  if constexpr (RING > 2) {
+    if (mine - i == 2) {
+      wait_vmcnt<kL>();
+      step(i++, slot);
+      slot = slot + 1 == RING ? 0 : slot + 1;
     }
   }
+  if (mine - i == 1) {
+    wait_vmcnt<0>();
+    step(i, slot);
+  }
 
-  if constexpr (kQuant) __syncthreads();  // the quantised rows are done with
-  typename MM::Acc* red = reinterpret_cast<typename MM::Acc*>(rows_smem);
-#pragma unroll
-  for (int i = 0; i < MB; i++)
-#pragma unroll
-    for (int j = 0; j < NB; j++) red[(wave * kTiles + i * NB + j) * 64 + lane] = acc[i][j];
+  __syncthreads();  // every ring is done with
+  typename MM::Acc* red = reinterpret_cast<typename MM::Acc*>(smem);
+  red[wave * 64 + lane] = acc;
   __syncthreads();
-  constexpr int kOut = kGated ? MB : kTiles;  // output blocks of 16 x 16
-  if (wave >= kOut) return;
-  auto total = [&](int tile) -> typename MM::Acc {
-    typename MM::Acc v = red[tile * 64 + lane];
+  if (wave > 0) return;
+  // weight rows 4 kg .. + 3; gated: of the lanes kg < 2 the gate rows, the up rows 8 on
+  auto total_of = [&](int l) -> typename MM::Acc {
+    typename MM::Acc v = red[l];
 #pragma unroll
-    for (int k = 1; k < WAVES; k++) v += red[(k * kTiles + tile) * 64 + lane];
+    for (int k = 1; k < W; k++) v += red[k * 64 + l];
     return v;
   };
-  const int i = kGated ? wave : wave / NB, j = kGated ? 0 : wave % NB;
-  const int m = 16 * i + lr, n = n0 + 16 * j + 4 * kg;
-  if (m >= p.M || n >= p.N) return;  // N % 8 == 0: four columns are in or out together
+  const int m = lr, n = n0 + 4 * kg;
+  if (m >= p.M || n >= p.N || (kGated && kg >= 2)) return;  // N % 8 == 0: four columns are in or out together
   float sa = 1.0f;
   if constexpr (kInt8) sa = kQuant ? row_scale[m] : p.sa[m];
   auto scaled = [&](const typename MM::Acc& v, int64_t col) -> float4 {
@@ -185,9 +177,9 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES / 4)
       return make_float4(v[0], v[1], v[2], v[3]);
     }
   };
-  float4 v = scaled(total(i * NB + j), n);
+  float4 v = scaled(total_of(lane), n);
   if constexpr (kGated) {
-    const float4 u = scaled(total(i * NB + 1), (int64_t)p.N + n);
+    const float4 u = scaled(total_of(lane + 32), (int64_t)p.N + n);
     if (!kInt8 && p.gate_up) {
       *reinterpret_cast<float4*>(p.gate_up + (int64_t)m * 2 * p.N + n) = v;
       *reinterpret_cast<float4*>(p.gate_up + (int64_t)m * 2 * p.N + p.N + n) = u;
@@ -205,33 +197,24 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES / 4)
 // Whether a product of M rows runs on rows_gemm.
 inline bool rows_ok(int64_t M) { return M <= kRowsMaxM; }
 
-template <bool kInt8, int EPI, int MB, int NB, bool kQuant>
-hipError_t launch_rows_shape(const TileArgs& a, const uint16_t* x, hipStream_t stream) {
-  constexpr int kPer = EPI == kTileGated ? 16 : 16 * NB;
+template <bool kInt8, int EPI>
+hipError_t launch_rows(const TileArgs& a, hipStream_t stream) {
+  constexpr int kPer = EPI == kTileGated ? 8 : 16;
   const unsigned grid = (unsigned)((a.N + kPer - 1) / kPer);
-  const size_t quant = kQuant ? (size_t)a.M * a.kend : 0;
-  auto lds = [&](int waves) { return std::max(quant, (size_t)waves * MB * NB * 1024); };
-  // waves: as many as have a whole round of steps each; four operand blocks take
-  // more registers than 16 waves have
-  const int64_t steps = a.kend / kRowsStep;
-  if constexpr (MB * NB < 4) {
-    if (steps >= 16 * kRowsUnroll) {
-      rows_gemm<kInt8, EPI, MB, NB, 16, kQuant><<<grid, 1024, lds(16), stream>>>(a, x);
-      return hipGetLastError();
-    }
-  }
-  if (steps >= 4 * kRowsUnroll)
-    rows_gemm<kInt8, EPI, MB, NB, 8, kQuant><<<grid, 512, lds(8), stream>>>(a, x);
+  if (a.M <= 8)
+    rows_gemm<kInt8, EPI, 1><<<grid, 64 * kRowsWaves, 0, stream>>>(a, nullptr);
   else
-    rows_gemm<kInt8, EPI, MB, NB, 4, kQuant><<<grid, 256, lds(4), stream>>>(a, x);
+    rows_gemm<kInt8, EPI, 2><<<grid, 64 * kRowsWaves, 0, stream>>>(a, nullptr);
   return hipGetLastError();
 }
 
-template <bool kInt8, int EPI>
-hipError_t launch_rows(const TileArgs& a, hipStream_t stream) {
-  constexpr int NB = EPI == kTileGated ? 2 : 1;
-  if (a.M <= 16) return launch_rows_shape<kInt8, EPI, 1, NB, false>(a, nullptr, stream);
-  return launch_rows_shape<kInt8, EPI, 2, NB, false>(a, nullptr, stream);
+// 8-bit, the activations x in bf16 (a.M <= 4, whole 128-byte steps of codes within
+// kRowsQuantBytes).
+inline bool rows_quant_ok(int64_t M, int64_t K) { return M <= 4 && M * ((K + 127) / 128 * 128) <= kRowsQuantBytes; }
+
+inline hipError_t launch_rows_quant(const TileArgs& a, const uint16_t* x, hipStream_t stream) {
+  rows_gemm<true, kTileStore, 0><<<(unsigned)((a.N + 15) / 16), 64 * kRowsWaves, 0, stream>>>(a, x);
+  return hipGetLastError();
 }
 
 }  // namespace
