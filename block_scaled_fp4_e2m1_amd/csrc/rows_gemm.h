@@ -1,7 +1,7 @@
-// Products of few rows (M <= 16), bound by the weight's bytes.
+// Products of few rows (M <= 64), bound by the weight's bytes.
 //
 // A workgroup owns 16 weight rows (gated: 8 gate rows and their 8 up rows) and all M
-// activation rows; its eight waves take the 128-byte steps of K in turn.  Each wave
+// activation rows; its waves take the 128-byte steps of K in turn.  Each wave
 // runs a ring of its own in LDS, filled by direct loads of eight rows x 128 bytes, so
 // there is no barrier until the waves' sums meet at the end.  The loads go through
 // LDS, though every byte is used by one wave only, because the memory pipeline
@@ -25,25 +25,29 @@
 namespace bsfp4 {
 namespace {
 
-constexpr int kRowsMaxM = 16;
-constexpr int kRowsWaves = 8;
+constexpr int kRowsMaxM = 64;
 constexpr int kRowsQuantBytes = 28 * 1024;  // quantised activations kept in LDS
 
-// Ring slots per wave: two workgroups per compute unit (80 KB each).
+// AQ: 1 KB loads of activations per step, eight rows each (1, 2, 4 or 8); 0: kQuant.
+// Waves and ring slots per wave so that two workgroups share a compute unit (80 KB
+// each).
 template <int AQ>
-constexpr int rows_ring() { return AQ == 2 ? 2 : 3; }
-template <int AQ>
-constexpr int rows_slot() { return (2 + AQ) * 1024; }
+struct RowsShape {
+  static constexpr int kWaves = AQ <= 2 ? 8 : 4;
+  static constexpr int kRing = AQ == 2 || AQ == 8 ? 2 : 3;
+  static constexpr int kSlot = (2 + AQ) * 1024;
+  static constexpr int kBlocks = AQ <= 2 ? 1 : AQ / 2;  // of 16 activation rows
+};
 
-// AQ: 1 KB loads of activations per step (1: M <= 8, 2: M <= 16, 0: kQuant).
 // p as for tile_gemm (operands along K), splits unused.
 template <bool kInt8, int EPI, int AQ>
-__global__ void __launch_bounds__(64 * kRowsWaves, 4)
+__global__ void __launch_bounds__(64 * RowsShape<AQ>::kWaves, RowsShape<AQ>::kWaves / 2)
     rows_gemm(const TileArgs p, const uint16_t* __restrict__ x) {
   typedef Mma<kInt8> MM;
   constexpr bool kGated = EPI == kTileGated, kQuant = AQ == 0;
   static_assert(!kQuant || (kInt8 && !kGated), "fused quantiser");
-  constexpr int W = kRowsWaves, RING = rows_ring<AQ>(), kSlot = rows_slot<AQ>(), kL = 2 + AQ;
+  constexpr int W = RowsShape<AQ>::kWaves, RING = RowsShape<AQ>::kRing, kSlot = RowsShape<AQ>::kSlot, kL = 2 + AQ,
+                MB = RowsShape<AQ>::kBlocks;
   constexpr int kRings = W * RING * kSlot;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[kRings + (kQuant ? kRowsQuantBytes : 0)];
   __shared__ int red_max[kQuant ? 4 * W : 1];
@@ -58,13 +62,17 @@ __global__ void __launch_bounds__(64 * kRowsWaves, 4)
   const v4u32 rw0 = make_rsrc4(p.B + (int64_t)n0 * p.ldb, (int64_t)min(kGated ? 8 : 16, p.N - n0) * p.ldb);
   const v4u32 rw1 = kGated ? make_rsrc4(p.B + ((int64_t)p.N + n0) * p.ldb, 8 * p.ldb) : rw0;
   const v4u32 ra = make_rsrc4(p.A, (int64_t)p.M * p.lda);
-  uint32_t c16[2], ow[2], oa[2];
+  uint32_t c16[2], ow[2], oa[AQ > 0 ? AQ : 1];
 #pragma unroll
   for (int q = 0; q < 2; q++) {
     const int r = 8 * q + row8;
     c16[q] = (uint32_t)((lane & 7) ^ tile_swz(r)) * 16;
     ow[q] = (uint32_t)((kGated ? row8 : r) * p.ldb) + c16[q];
-    oa[q] = r < p.M ? (uint32_t)(r * p.lda) + c16[q] : kBufOOB;
+  }
+#pragma unroll
+  for (int q = 0; q < AQ; q++) {
+    const int r = 8 * q + row8;
+    oa[q] = r < p.M ? (uint32_t)(r * p.lda) + c16[q & 1] : kBufOOB;
   }
   const uint32_t ring0 = lds_offset(smem) + (uint32_t)wave * RING * kSlot;
   const uint8_t* const ring = smem + wave * RING * kSlot;
@@ -75,13 +83,21 @@ __global__ void __launch_bounds__(64 * kRowsWaves, 4)
     for (int q = 0; q < 2; q++)
       buf_lds16(q ? rw1 : rw0, (int)c16[q] < left ? ow[q] : kBufOOB, soff, lds + q * 1024);
 #pragma unroll
-    for (int q = 0; q < AQ; q++) buf_lds16(ra, (int)c16[q] < left ? oa[q] : kBufOOB, soff, lds + (2 + q) * 1024);
+    for (int q = 0; q < AQ; q++) buf_lds16(ra, (int)c16[q & 1] < left ? oa[q] : kBufOOB, soff, lds + (2 + q) * 1024);
   };
   const int total = (kb + kTileStage - 1) / kTileStage;
-  const int mine = wave < total ? (total - 1 - wave) / W + 1 : 0;  // steps wave, wave + W, ...
+  const int mine = wave < total ? (total - 1 - wave) / W + 1 : 0;  // turns wave, wave + W, ...
+  // Each workgroup begins a step further on in K: rows of 4096 bytes and the like put
+  // one step of every row on the same few memory channels (int8 16 x 4096 x 14336
+  // 13.5 us with one start for all, 10.7 so).
+  const int first = (int)(blockIdx.x % (unsigned)total);
+  auto step_of = [&](int i) {
+    const int s = wave + i * W + first;
+    return s < total ? s : s - total;
+  };
 #pragma unroll
   for (int r = 0; r < RING; r++)
-    if (r < mine) issue(wave + r * W, r);
+    if (r < mine) issue(step_of(r), r);
 
   if constexpr (kQuant) {
     // all M <= 4 rows, a chunk of eight values at a time; a row's codes are kept in
@@ -109,30 +125,34 @@ __global__ void __launch_bounds__(64 * kRowsWaves, 4)
     asm volatile("" ::: "memory");
   }
 
-  typename MM::Acc acc{};
+  typename MM::Acc acc[MB] = {};
   // lane offsets of the two K halves of a step: row lr, chunk 4 h + kg
   uint32_t off[2];
 #pragma unroll
   for (int h = 0; h < 2; h++) off[h] = (uint32_t)(lr * kTileStage + (((4 * h + kg) ^ tile_swz(lr)) * 16));
   auto step = [&](int i, int slot) {
     const uint8_t* s = ring + slot * kSlot;
-    v4i w[2], a[2];
+    v4i w[2], a[2][MB];
 #pragma unroll
     for (int h = 0; h < 2; h++) {
       w[h] = *reinterpret_cast<const v4i*>(s + off[h]);
       if constexpr (kQuant) {
-        const int at = min(lr, p.M - 1) * total * kTileStage + (wave + i * W) * kTileStage + h * 64 + kg * 16;
-        a[h] = *reinterpret_cast<const v4i*>(smem + kRings + at);
+        const int at = min(lr, p.M - 1) * total * kTileStage + step_of(i) * kTileStage + h * 64 + kg * 16;
+        a[h][0] = *reinterpret_cast<const v4i*>(smem + kRings + at);
       } else {
         // M <= 8: the upper eight rows of the fragment repeat the lower (outputs not stored)
-        a[h] = *reinterpret_cast<const v4i*>(s + 2048 + (AQ == 1 ? off[h] & 1023u : off[h]));
+#pragma unroll
+        for (int b = 0; b < MB; b++)
+          a[h][b] = *reinterpret_cast<const v4i*>(s + 2048 + b * 2048 + (AQ == 1 ? off[h] & 1023u : off[h]));
       }
     }
     // the fragments are in registers before the slot is filled again
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    if (i + RING < mine) issue(wave + (i + RING) * W, slot);
+    if (i + RING < mine) issue(step_of(i + RING), slot);
 #pragma unroll
-    for (int h = 0; h < 2; h++) acc = MM::run(w[h], a[h], acc);
+    for (int h = 0; h < 2; h++)
+#pragma unroll
+      for (int b = 0; b < MB; b++) acc[b] = MM::run(w[h], a[h][b], acc[b]);
   };
   int i = 0, slot = 0;
   for (; i + RING <= mine; i++) {
@@ -154,17 +174,18 @@ __global__ void __launch_bounds__(64 * kRowsWaves, 4)
 
   __syncthreads();  // every ring is done with
   typename MM::Acc* red = reinterpret_cast<typename MM::Acc*>(smem);
-  red[wave * 64 + lane] = acc;
+#pragma unroll
+  for (int b = 0; b < MB; b++) red[(wave * MB + b) * 64 + lane] = acc[b];
   __syncthreads();
-  if (wave > 0) return;
+  if (wave >= MB) return;  // wave b finishes activation rows 16 b .. + 15
   // weight rows 4 kg .. + 3; gated: of the lanes kg < 2 the gate rows, the up rows 8 on
   auto total_of = [&](int l) -> typename MM::Acc {
-    typename MM::Acc v = red[l];
+    typename MM::Acc v = red[wave * 64 + l];
 #pragma unroll
-    for (int k = 1; k < W; k++) v += red[k * 64 + l];
+    for (int k = 1; k < W; k++) v += red[(k * MB + wave) * 64 + l];
     return v;
   };
-  const int m = lr, n = n0 + 4 * kg;
+  const int m = 16 * wave + lr, n = n0 + 4 * kg;
   if (m >= p.M || n >= p.N || (kGated && kg >= 2)) return;  // N % 8 == 0: four columns are in or out together
   float sa = 1.0f;
   if constexpr (kInt8) sa = kQuant ? row_scale[m] : p.sa[m];
@@ -194,26 +215,34 @@ __global__ void __launch_bounds__(64 * kRowsWaves, 4)
       make_uint2(pack_bf16x2_ieee(v.x, v.y), pack_bf16x2_ieee(v.z, v.w));
 }
 
-// Whether a product of M rows runs on rows_gemm.
-inline bool rows_ok(int64_t M) { return M <= kRowsMaxM; }
+template <bool kInt8, int EPI, int AQ>
+void launch_rows_shape(const TileArgs& a, const uint16_t* x, hipStream_t stream) {
+  constexpr int kPer = EPI == kTileGated ? 8 : 16;
+  rows_gemm<kInt8, EPI, AQ>
+      <<<(unsigned)((a.N + kPer - 1) / kPer), 64 * RowsShape<AQ>::kWaves, 0, stream>>>(a, x);
+}
 
 template <bool kInt8, int EPI>
 hipError_t launch_rows(const TileArgs& a, hipStream_t stream) {
-  constexpr int kPer = EPI == kTileGated ? 8 : 16;
-  const unsigned grid = (unsigned)((a.N + kPer - 1) / kPer);
-  if (a.M <= 8)
-    rows_gemm<kInt8, EPI, 1><<<grid, 64 * kRowsWaves, 0, stream>>>(a, nullptr);
-  else
-    rows_gemm<kInt8, EPI, 2><<<grid, 64 * kRowsWaves, 0, stream>>>(a, nullptr);
+  if (a.M <= 8) launch_rows_shape<kInt8, EPI, 1>(a, nullptr, stream);
+  else if (a.M <= 16) launch_rows_shape<kInt8, EPI, 2>(a, nullptr, stream);
+  else if (a.M <= 32) launch_rows_shape<kInt8, EPI, 4>(a, nullptr, stream);
+  else launch_rows_shape<kInt8, EPI, 8>(a, nullptr, stream);
   return hipGetLastError();
 }
+
+// Whether a product of M rows with n weight rows (gated: both halves) runs on
+// rows_gemm.  Every workgroup reads all activation rows, so past M n = 2^18 the tiles
+// are faster: int8 16 x 4096 x 14336 10.7 us against 11.0, 32 x 4096 x 14336 11.9
+// against 11.2; 32 x 4096 x 8192 7.3 against 9.8; 64 x 7168 x 4096 9.0 against 10.8.
+inline bool rows_ok(int64_t M, int64_t n) { return M <= kRowsMaxM && M * n <= ((int64_t)1 << 18); }
 
 // 8-bit, the activations x in bf16 (a.M <= 4, whole 128-byte steps of codes within
 // kRowsQuantBytes).
 inline bool rows_quant_ok(int64_t M, int64_t K) { return M <= 4 && M * ((K + 127) / 128 * 128) <= kRowsQuantBytes; }
 
 inline hipError_t launch_rows_quant(const TileArgs& a, const uint16_t* x, hipStream_t stream) {
-  rows_gemm<true, kTileStore, 0><<<(unsigned)((a.N + 15) / 16), 64 * kRowsWaves, 0, stream>>>(a, x);
+  launch_rows_shape<true, kTileStore, 0>(a, x, stream);
   return hipGetLastError();
 }
 
