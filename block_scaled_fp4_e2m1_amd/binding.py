@@ -421,10 +421,31 @@ def _act(act) -> int:
         raise ValueError(f"unknown activation {act!r} (one of {', '.join(ACTIVATIONS)})") from None
 
 
-def _out(t, shape, dtype, name):
-    if t is not None:
+# A call's checks and marshalling are most of what a decode step waits for (the kernels take 3 to 6 us): each
+# argument is one combined test, the detailed checks only run to name what it found wrong.
+
+_BF16, _I8, _F32 = torch.bfloat16, torch.int8, torch.float32
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _as(t, dtype, shape, name):
+    """t is a contiguous tensor of this type and shape."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
         _need(t, dtype, name)
         _shape(t, shape, name)
+
+
+def _opt(t, dtype, shape, name):
+    if t is not None:
+        _as(t, dtype, shape, name)
+
+
+def _matrix(t, dtype, name):
+    """Rows and columns of a contiguous matrix of this type."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == 2 and t.is_contiguous()):
+        _need(t, dtype, name)
+        _dims(t, 2, name)
+    return t.shape
 
 
 def _multiple(v, step, name):
@@ -432,147 +453,130 @@ def _multiple(v, step, name):
         raise ValueError(f"{name}={v} is not a multiple of {step}")
 
 
+def _gpu(names, *tensors):
+    """The one GPU all given tensors are on; `names` one word each."""
+    index, first = -1, None
+    for i, t in enumerate(tensors):
+        if t is not None:
+            d = t.get_device() if t.is_cuda else -1
+            if d != index or d < 0:
+                if d < 0 or first is not None:
+                    return _device(*zip(tensors, names.split()))  # says which
+                index, first = d, t
+    return first.device
+
+
 def _a(t):
     """A tensor's address as ctypes takes it fastest."""
     return None if t is None else t.data_ptr()
 
 
-def _launch(dev, what, fn, *args):
-    """fn(*args, stream) with the tensors' device as the current one, on its current stream."""
-    if torch.cuda.current_device() == dev.index:
-        status = fn(*args, _stream(dev))
-    else:
+def _run(dev, what, fn, args, size_fn=None, sizes=()):
+    """fn(*args, [workspace, its bytes,] stream) with the tensors' device as the current one, on its current
+    stream; the workspace's size is planned for that device too."""
+    if _current_device() != dev.index:
         with torch.cuda.device(dev):
-            status = fn(*args, _stream(dev))
+            return _run(dev, what, fn, args, size_fn, sizes)
+    stream = _raw_stream(dev.index) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+    if size_fn is None:
+        status = fn(*args, stream)
+    else:
+        n = size_fn(*sizes)
+        ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+        status = fn(*args, _a(ws), n, stream)
     if status != 0:
         _check(status, what)
-
-
-def _ws_bytes(dev, fn, *sizes) -> int:
-    """A workspace size; the plan behind it goes by the tensors' device."""
-    if torch.cuda.current_device() == dev.index:
-        return fn(*sizes)
-    with torch.cuda.device(dev):
-        return fn(*sizes)
-
-
-def _call(dev, what, fn, args, size_fn, sizes):
-    """_launch with the workspace that the call needs."""
-    n = _ws_bytes(dev, size_fn, *sizes)
-    ws = _workspace(n, dev)
-    _launch(dev, what, fn, *args, _a(ws), n)
 
 
 def int8_quantize(x: torch.Tensor, q: torch.Tensor | None = None, s: torch.Tensor | None = None):
     """bf16 [M, K] -> (8-bit rows int8 [M, K], scales float32 [M]), x ~ q * s per row (token):
     s = max|x| / 127, q = round-to-even(127 x / max|x|)."""
-    _need(x, torch.bfloat16, "x")
-    _dims(x, 2, "x")
-    M, K = x.shape
+    M, K = _matrix(x, _BF16, "x")
     _multiple(K, 8, "K")
-    _out(q, (M, K), torch.int8, "q")
-    _out(s, (M,), torch.float32, "s")
-    dev = _device((x, "x"), (q, "q"), (s, "s"))
+    _opt(q, _I8, (M, K), "q")
+    _opt(s, _F32, (M,), "s")
+    dev = _gpu("x q s", x, q, s)
     if q is None:
-        q = torch.empty((M, K), dtype=torch.int8, device=dev)
+        q = torch.empty_like(x, dtype=_I8)
     if s is None:
-        s = torch.empty(M, dtype=torch.float32, device=dev)
-    _launch(dev, "bsfp4_int8_quantize", load().bsfp4_int8_quantize, _a(x), M, K, _a(q), _a(s))
+        s = x.new_empty(M, dtype=_F32)
+    _run(dev, "bsfp4_int8_quantize", load().bsfp4_int8_quantize, (x.data_ptr(), M, K, q.data_ptr(), s.data_ptr()))
     return q, s
 
 
 def _int8_weight(B, SB, K, name, sname):
-    _need(B, torch.int8, name)
-    _need(SB, torch.float32, sname)
-    _dims(B, 2, name)
-    if B.shape[1] != K:
-        raise ValueError(f"the activations have K={K} but {name} has K={B.shape[1]}")
+    N, KB = _matrix(B, _I8, name)
+    if KB != K:
+        raise ValueError(f"the activations have K={K} but {name} has K={KB}")
     _multiple(K, 16, "K")
-    _shape(SB, (B.shape[0],), sname)
-
-
-def _int8_bias(bias, N):
-    if bias is not None:
-        _need(bias, torch.bfloat16, "bias")
-        _shape(bias, (N,), "bias")
+    _as(SB, _F32, (N,), sname)
+    return N
 
 
 def int8_gemm(A, SA, B, SB, bias: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
     """D = bf16((A @ B^T) * SA[:, None] * SB + bias); A int8 [M, K], SA [M], B int8 [N, K], SB [N]."""
-    _need(A, torch.int8, "A")
-    _need(SA, torch.float32, "SA")
-    _dims(A, 2, "A")
-    M, K = A.shape
-    _int8_weight(B, SB, K, "B", "SB")
-    N = B.shape[0]
+    M, K = _matrix(A, _I8, "A")
+    N = _int8_weight(B, SB, K, "B", "SB")
     _multiple(N, 8, "N")
-    _shape(SA, (M,), "SA")
-    _int8_bias(bias, N)
-    _out(out, (M, N), torch.bfloat16, "out")
-    dev = _device((A, "A"), (SA, "SA"), (B, "B"), (SB, "SB"), (bias, "bias"), (out, "out"))
-    D = out if out is not None else torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    _as(SA, _F32, (M,), "SA")
+    _opt(bias, _BF16, (N,), "bias")
+    _opt(out, _BF16, (M, N), "out")
+    dev = _gpu("A SA B SB bias out", A, SA, B, SB, bias, out)
+    D = out if out is not None else A.new_empty((M, N), dtype=_BF16)
     lib = load()
-    _call(dev, "bsfp4_int8_gemm", lib.bsfp4_int8_gemm,
-          (_a(A), _a(SA), _a(B), _a(SB), _a(bias), _a(D), M, N, K), lib.bsfp4_int8_gemm_workspace_size, (M, N, K))
+    _run(dev, "bsfp4_int8_gemm", lib.bsfp4_int8_gemm,
+         (A.data_ptr(), SA.data_ptr(), B.data_ptr(), SB.data_ptr(), _a(bias), D.data_ptr(), M, N, K),
+         lib.bsfp4_int8_gemm_workspace_size, (M, N, K))
     return D
 
 
 def int8_quantize_gemm(x, B, SB, bias: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
     """D = int8_gemm(*int8_quantize(x), B, SB, bias) in one call; x bf16 [M, K]."""
-    _need(x, torch.bfloat16, "x")
-    _dims(x, 2, "x")
-    M, K = x.shape
-    _int8_weight(B, SB, K, "B", "SB")
-    N = B.shape[0]
+    M, K = _matrix(x, _BF16, "x")
+    N = _int8_weight(B, SB, K, "B", "SB")
     _multiple(N, 8, "N")
-    _int8_bias(bias, N)
-    _out(out, (M, N), torch.bfloat16, "out")
-    dev = _device((x, "x"), (B, "B"), (SB, "SB"), (bias, "bias"), (out, "out"))
-    D = out if out is not None else torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    _opt(bias, _BF16, (N,), "bias")
+    _opt(out, _BF16, (M, N), "out")
+    dev = _gpu("x B SB bias out", x, B, SB, bias, out)
+    D = out if out is not None else x.new_empty((M, N))
     lib = load()
-    _call(dev, "bsfp4_int8_quantize_gemm", lib.bsfp4_int8_quantize_gemm,
-          (_a(x), _a(B), _a(SB), _a(bias), _a(D), M, N, K), lib.bsfp4_int8_quantize_gemm_workspace_size, (M, N, K))
+    _run(dev, "bsfp4_int8_quantize_gemm", lib.bsfp4_int8_quantize_gemm,
+         (x.data_ptr(), B.data_ptr(), SB.data_ptr(), _a(bias), D.data_ptr(), M, N, K),
+         lib.bsfp4_int8_quantize_gemm_workspace_size, (M, N, K))
     return D
 
 
-def _gated_rows(W13, name="W13") -> int:
-    if W13.shape[0] % 2:
-        raise ValueError(f"{name} must hold gate rows and as many up rows, got {W13.shape[0]} rows")
-    I = W13.shape[0] // 2
-    _multiple(I, 8, "I")
-    return I
+def _gated_rows(rows, name="W13") -> int:
+    if rows % 2:
+        raise ValueError(f"{name} must hold gate rows and as many up rows, got {rows} rows")
+    _multiple(rows // 2, 8, "I")
+    return rows // 2
 
 
 def int8_gated_ffn(A, SA, W13, SW13, act="silu", out: torch.Tensor | None = None) -> torch.Tensor:
     """h = bf16(act(G) * U), [G | U] = (A @ W13^T) * SA[:, None] * SW13; A int8 [M, K], W13 int8 [2 I, K]
     (gate rows, then up rows)."""
     a = _act(act)
-    _need(A, torch.int8, "A")
-    _need(SA, torch.float32, "SA")
-    _dims(A, 2, "A")
-    M, K = A.shape
-    _int8_weight(W13, SW13, K, "W13", "SW13")
-    I = _gated_rows(W13)
-    _shape(SA, (M,), "SA")
-    _out(out, (M, I), torch.bfloat16, "out")
-    dev = _device((A, "A"), (SA, "SA"), (W13, "W13"), (SW13, "SW13"), (out, "out"))
-    h = out if out is not None else torch.empty((M, I), dtype=torch.bfloat16, device=dev)
+    M, K = _matrix(A, _I8, "A")
+    I = _gated_rows(_int8_weight(W13, SW13, K, "W13", "SW13"))
+    _as(SA, _F32, (M,), "SA")
+    _opt(out, _BF16, (M, I), "out")
+    dev = _gpu("A SA W13 SW13 out", A, SA, W13, SW13, out)
+    h = out if out is not None else A.new_empty((M, I), dtype=_BF16)
     lib = load()
-    _call(dev, "bsfp4_int8_gated_ffn", lib.bsfp4_int8_gated_ffn,
-          (_a(A), _a(SA), _a(W13), _a(SW13), a, _a(h), M, I, K), lib.bsfp4_int8_gated_ffn_workspace_size, (M, I, K))
+    _run(dev, "bsfp4_int8_gated_ffn", lib.bsfp4_int8_gated_ffn,
+         (A.data_ptr(), SA.data_ptr(), W13.data_ptr(), SW13.data_ptr(), a, h.data_ptr(), M, I, K),
+         lib.bsfp4_int8_gated_ffn_workspace_size, (M, I, K))
     return h
 
 
 def _gated_args(x, W13):
-    _need(x, torch.bfloat16, "x")
-    _need(W13, torch.bfloat16, "W13")
-    _dims(x, 2, "x")
-    _dims(W13, 2, "W13")
-    M, H = x.shape
-    if W13.shape[1] != H:
-        raise ValueError(f"x has H={H} but W13 has H={W13.shape[1]}")
+    M, H = _matrix(x, _BF16, "x")
+    rows, HW = _matrix(W13, _BF16, "W13")
+    if HW != H:
+        raise ValueError(f"x has H={H} but W13 has H={HW}")
     _multiple(H, 8, "H")
-    return M, H, _gated_rows(W13)
+    return M, H, _gated_rows(rows)
 
 
 def gated_ffn(x, W13, act="silu", save_gate_up: bool = False, out: torch.Tensor | None = None):
@@ -580,13 +584,14 @@ def gated_ffn(x, W13, act="silu", save_gate_up: bool = False, out: torch.Tensor 
     With save_gate_up returns (h, float32 [G | U]) for gated_ffn_backward."""
     a = _act(act)
     M, H, I = _gated_args(x, W13)
-    _out(out, (M, I), torch.bfloat16, "out")
-    dev = _device((x, "x"), (W13, "W13"), (out, "out"))
-    h = out if out is not None else torch.empty((M, I), dtype=torch.bfloat16, device=dev)
-    gate_up = torch.empty((M, 2 * I), dtype=torch.float32, device=dev) if save_gate_up else None
+    _opt(out, _BF16, (M, I), "out")
+    dev = _gpu("x W13 out", x, W13, out)
+    h = out if out is not None else x.new_empty((M, I))
+    gate_up = x.new_empty((M, 2 * I), dtype=_F32) if save_gate_up else None
     lib = load()
-    _call(dev, "bsfp4_gated_ffn", lib.bsfp4_gated_ffn, (_a(x), _a(W13), a, _a(h), _a(gate_up), M, I, H),
-          lib.bsfp4_gated_ffn_workspace_size, (M, I, H))
+    _run(dev, "bsfp4_gated_ffn", lib.bsfp4_gated_ffn,
+         (x.data_ptr(), W13.data_ptr(), a, h.data_ptr(), _a(gate_up), M, I, H),
+         lib.bsfp4_gated_ffn_workspace_size, (M, I, H))
     return (h, gate_up) if save_gate_up else h
 
 
@@ -595,45 +600,39 @@ def gated_ffn_backward(dh, x, W13, gate_up, act="silu", need_dx: bool = True, ne
     (float32 [M, 2 I]), the rest bf16; None for one that is not needed."""
     a = _act(act)
     M, H, I = _gated_args(x, W13)
-    _need(dh, torch.bfloat16, "dh")
-    _shape(dh, (M, I), "dh")
-    _need(gate_up, torch.float32, "gate_up")
-    _shape(gate_up, (M, 2 * I), "gate_up")
-    dev = _device((dh, "dh"), (x, "x"), (W13, "W13"), (gate_up, "gate_up"))
-    dx = torch.empty((M, H), dtype=torch.bfloat16, device=dev) if need_dx else None
-    dW = torch.empty((2 * I, H), dtype=torch.bfloat16, device=dev) if need_dW13 else None
+    _as(dh, _BF16, (M, I), "dh")
+    _as(gate_up, _F32, (M, 2 * I), "gate_up")
+    dev = _gpu("dh x W13 gate_up", dh, x, W13, gate_up)
+    dx = torch.empty_like(x) if need_dx else None
+    dW = torch.empty_like(W13) if need_dW13 else None
     if dx is None and dW is None:
         return None, None
     lib = load()
-    _call(dev, "bsfp4_gated_ffn_backward", lib.bsfp4_gated_ffn_backward,
-          (_a(dh), _a(x), _a(W13), _a(gate_up), a, _a(dx), _a(dW), M, I, H),
-          lib.bsfp4_gated_ffn_backward_workspace_size, (M, I, H))
+    _run(dev, "bsfp4_gated_ffn_backward", lib.bsfp4_gated_ffn_backward,
+         (dh.data_ptr(), x.data_ptr(), W13.data_ptr(), gate_up.data_ptr(), a, _a(dx), _a(dW), M, I, H),
+         lib.bsfp4_gated_ffn_backward_workspace_size, (M, I, H))
     return dx, dW
 
 
 def _norm_args(x, rows, rows_name, w_post, w_pre, gate, eps):
     """Checks what forward and backward share; `rows` is the [T, H] tensor that is always there.  (T, H, groups)"""
-    _need(rows, torch.bfloat16, rows_name)
-    _dims(rows, 2, rows_name)
-    T, H = rows.shape
+    T, H = _matrix(rows, _BF16, rows_name)
     _multiple(H, 8, "H")
     groups = 1
     if x is not None:
-        _need(x, torch.bfloat16, "x")
-        _shape(x, (T, H), "x")
+        _as(x, _BF16, (T, H), "x")
     elif w_post is not None or gate is not None:
         raise ValueError("without x there is no w_post and no gate")
     elif w_pre is None:
         raise ValueError("neither x nor w_pre is given")
-    for w, n in ((w_post, "w_post"), (w_pre, "w_pre")):
-        if w is not None:
-            _need(w, torch.bfloat16, n)
-            _shape(w, (H,), n)
+    _opt(w_post, _BF16, (H,), "w_post")
+    _opt(w_pre, _BF16, (H,), "w_pre")
     if gate is not None:
-        _need(gate, torch.bfloat16, "gate")
-        if gate.dim() not in (1, 2) or gate.shape[-1] != H:
-            raise ValueError(f"gate must have shape ({H},) or (groups, {H}), got {tuple(gate.shape)}")
-        groups = 1 if gate.dim() == 1 else gate.shape[0]
+        _need(gate, _BF16, "gate")
+        shape = gate.shape
+        if len(shape) not in (1, 2) or shape[-1] != H:
+            raise ValueError(f"gate must have shape ({H},) or (groups, {H}), got {tuple(shape)}")
+        groups = 1 if len(shape) == 1 else shape[0]
         if groups == 0 or T % groups:
             raise ValueError(f"the {T} rows are not a multiple of the {groups} gate rows")
     if not 0.0 < eps < 1e30:
@@ -662,9 +661,8 @@ def block_norm(x, residual, w_post=None, w_pre=None, gate=None, scale: float = 1
         raise ValueError("fmt='int8' needs w_pre")
     if res_out is not None and x is None:
         raise ValueError("without x nothing is written to res_out")
-    _out(res_out, (T, H), torch.bfloat16, "res_out")
-    dev = _device((residual, "residual"), (x, "x"), (w_post, "w_post"), (w_pre, "w_pre"), (gate, "gate"),
-                  (res_out, "res_out"))
+    _opt(res_out, _BF16, (T, H), "res_out")
+    dev = _gpu("residual x w_post w_pre gate res_out", residual, x, w_post, w_pre, gate, res_out)
     res = residual
     if x is not None:
         res = res_out if res_out is not None else torch.empty_like(residual)
@@ -674,11 +672,11 @@ def block_norm(x, residual, w_post=None, w_pre=None, gate=None, scale: float = 1
         z = torch.empty_like(residual)
         outs = (z,)
     elif w_pre is not None:
-        q, s = residual.new_empty((T, H), dtype=torch.int8), residual.new_empty(T, dtype=torch.float32)
+        q, s = torch.empty_like(residual, dtype=_I8), residual.new_empty(T, dtype=_F32)
         outs = (q, s)
     args = _pack_norm(_z(x), residual.data_ptr(), _z(w_post), _z(w_pre), _z(gate), scale, eps, T, H, groups,
                       0 if x is None else res.data_ptr(), _z(z), _z(q), _z(s), 0, 0, 0, 0, 0, 0, 0)
-    _launch(dev, "bsfp4_block_norm", load().bsfp4_block_norm, args)
+    _run(dev, "bsfp4_block_norm", load().bsfp4_block_norm, (args,))
     return (res, *outs) if outs else res
 
 
@@ -695,18 +693,17 @@ def block_norm_backward(dres, dz, x, res, w_post=None, w_pre=None, gate=None, sc
         raise ValueError("dz without w_pre")
     if w_pre is None and dres is None:
         raise ValueError("without w_pre dres is needed")
-    for t, n in ((dres, "dres"), (dz, "dz")):
-        _out(t, (T, H), torch.bfloat16, n)
-    dev = _device((rows, "res"), (dres, "dres"), (dz, "dz"), (x, "x"), (w_post, "w_post"), (w_pre, "w_pre"),
-                  (gate, "gate"))
-    vec = lambda w: None if w is None else torch.empty_like(w, dtype=torch.float32)  # noqa: E731
+    _opt(dres, _BF16, (T, H), "dres")
+    _opt(dz, _BF16, (T, H), "dz")
+    dev = _gpu("res dres dz x w_post w_pre gate", rows, dres, dz, x, w_post, w_pre, gate)
+    vec = lambda w: None if w is None else torch.empty_like(w, dtype=_F32)  # noqa: E731
     dx, dresidual = (torch.empty_like(rows) if x is not None else None), torch.empty_like(rows)
     dw_post, dw_pre, dgate = vec(w_post), vec(w_pre), vec(gate)
     args = _pack_norm(_z(x), 0, _z(w_post), _z(w_pre), _z(gate), scale, eps, T, H, groups, _z(res), 0, 0, 0, _z(dres),
                       _z(dz), _z(dx), dresidual.data_ptr(), _z(dw_post), _z(dw_pre), _z(dgate))
     lib = load()
-    _call(dev, "bsfp4_block_norm_backward", lib.bsfp4_block_norm_backward, (args,),
-          lib.bsfp4_block_norm_backward_workspace_size, (T, H, groups))
+    _run(dev, "bsfp4_block_norm_backward", lib.bsfp4_block_norm_backward, (args,),
+         lib.bsfp4_block_norm_backward_workspace_size, (T, H, groups))
     return dx, dresidual, dw_post, dw_pre, dgate
 
 
