@@ -65,7 +65,7 @@ BwdPlan plan_bwd(int64_t M, int64_t H, int64_t I) {
 }  // namespace
 
 size_t gated_ffn_workspace(int64_t M, int64_t I, int64_t H) {
-  if (rows_ok(M, 2 * I)) return 0;
+  if (rows_ok(M, 2 * I, 2 * H)) return 0;
   return tile_workspace(plan_tile(M, 2 * I, 2 * H, device_cu_count()), M, 2 * I);
 }
 
@@ -82,7 +82,7 @@ hipError_t launch_gated_ffn(const uint16_t* x, const uint16_t* W, int act, uint1
   a.D = h;
   a.gate_up = gate_up;
   a.part = ws;
-  if (rows_ok(M, 2 * I)) return launch_rows<false, kTileGated>(a, stream);
+  if (rows_ok(M, 2 * I, 2 * H)) return launch_rows<false, kTileGated>(a, stream);
   return launch_tile<false, false, false, kTileGated>(a, plan_tile(M, 2 * I, 2 * H, device_cu_count()), stream);
 }
 

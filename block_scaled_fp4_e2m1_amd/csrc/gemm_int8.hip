@@ -10,7 +10,7 @@
 
 namespace bsfp4 {
 size_t int8_gemm_workspace(int64_t M, int64_t N, int64_t K) {
-  if (rows_ok(M, N)) return 0;
+  if (rows_ok(M, N, K)) return 0;
   return tile_workspace(plan_tile(M, N, K, device_cu_count()), M, N);
 }
 
@@ -46,7 +46,7 @@ hipError_t launch_int8_gemm(const int8_t* A, const float* sa, const int8_t* B, c
   a.bias = bias;
   a.D = D;
   a.part = ws;
-  if (rows_ok(M, N)) return launch_rows<true, kTileStore>(a, stream);
+  if (rows_ok(M, N, K)) return launch_rows<true, kTileStore>(a, stream);
   return launch_tile<true, false, false, kTileStore>(a, plan_tile(M, N, K, device_cu_count()), stream);
 }
 
@@ -64,7 +64,7 @@ hipError_t launch_int8_gated(const int8_t* A, const float* sa, const int8_t* W, 
   a.act = act;
   a.D = D;
   a.part = ws;
-  if (rows_ok(M, 2 * I)) return launch_rows<true, kTileGated>(a, stream);
+  if (rows_ok(M, 2 * I, K)) return launch_rows<true, kTileGated>(a, stream);
   return launch_tile<true, false, false, kTileGated>(a, plan_tile(M, 2 * I, K, device_cu_count()), stream);
 }
 

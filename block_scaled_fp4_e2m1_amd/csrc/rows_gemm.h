@@ -231,11 +231,18 @@ hipError_t launch_rows(const TileArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Whether a product of M rows with n weight rows (gated: both halves) runs on
-// rows_gemm.  Every workgroup reads all activation rows, so past M n = 2^18 the tiles
+// Whether a product of M rows with n weight rows (gated: both halves) of kbytes runs
+// on rows_gemm.  Every workgroup reads all activation rows, so past some M n the tiles
 // are faster: int8 16 x 4096 x 14336 10.7 us against 11.0, 32 x 4096 x 14336 11.9
 // against 11.2; 32 x 4096 x 8192 7.3 against 9.8; 64 x 7168 x 4096 9.0 against 10.8.
-inline bool rows_ok(int64_t M, int64_t n) { return M <= kRowsMaxM && M * n <= ((int64_t)1 << 18); }
+// Few rows keep it longer, where K has steps enough for the waves' rings (8 turns or
+// more of 128 bytes each): int8 8 x 131072 x 4096 96 against 114, 16 x 65536 x 4096 53
+// against 62, bf16 gated 1 x 32768 x 4096 48 against 61; but bf16 gated 16 x 131072 x
+// 4096 196 against 176, int8 4 x 131072 x 1024 35 against 27.
+inline bool rows_ok(int64_t M, int64_t n, int64_t kbytes) {
+  const bool few = M <= 16 && kbytes >= 4096;
+  return M <= kRowsMaxM && M * n <= ((int64_t)1 << (few ? 20 : 18));
+}
 
 // 8-bit, the activations x in bf16 (a.M <= 4, whole 128-byte steps of codes within
 // kRowsQuantBytes).

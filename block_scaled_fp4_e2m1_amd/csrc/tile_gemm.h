@@ -665,7 +665,8 @@ inline TilePlan plan_tile(int64_t M, int64_t N, int64_t kbytes, int cus) {
       consider(t, TilePlan{(TileKind)c, sp, 0, 0, kTile256});
     }
     // a part-filled last round (896 tiles of 256 x 256 on 256 units: 3.5 rounds) goes
-    // to smaller tiles: measured at 4096 x 14336 x 4096, gated, 365 -> 340 us
+    // to smaller tiles: bf16 gated with its sums kept, 4096 x 14336 x 4096, 420 -> 397
+    // us, a weight's gradient 14336 x 4096 x 4096 381 -> 367
     const int64_t full = all / slots * slots;
     if (c > kTile128 || full == 0 || full == all) continue;
     const int64_t tm = (M + cd.bm - 1) / cd.bm, tn = (N + cd.bn - 1) / cd.bn;
