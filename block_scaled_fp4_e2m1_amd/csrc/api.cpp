@@ -311,9 +311,9 @@ bsfp4_status check_rows_cols(const char* rows_name, int64_t M, const char* cols_
     return fail(BSFP4_ERR_SHAPE, "%s=%lld is not a multiple of %lld", cols_name, (long long)N, (long long)n_step);
   if (K % k_step)
     return fail(BSFP4_ERR_SHAPE, "%s=%lld is not a multiple of %lld", k_name, (long long)K, (long long)k_step);
+  if (M > ((int64_t)1 << 40) / N) return fail(BSFP4_ERR_SHAPE, "%s * %s exceeds 2^40", rows_name, cols_name);
   // a last tile's rows are counted past M: room for one tile
   if (M > INT32_MAX - 256 || N > (INT32_MAX - 256) / 2) return fail(BSFP4_ERR_SHAPE, "dimensions must fit in 31 bits");
-  if (M > ((int64_t)1 << 40) / N) return fail(BSFP4_ERR_SHAPE, "%s * %s exceeds 2^40", rows_name, cols_name);
   return BSFP4_OK;
 }
 

@@ -141,6 +141,7 @@ def test_abi_int8(lib):
     assert call(K=131072) == SHAPE and "131056" in err(lib)
     assert call(M=1 << 31) == SHAPE
     assert call(M=(1 << 31) - 1, N=1 << 20) == SHAPE and "2^40" in err(lib)
+    assert call(M=(1 << 31) - 1) == SHAPE and "31 bits" in err(lib)  # a tile's rows are counted past M
     assert call(A=None) == INVALID and call(sb=None) == INVALID and call(D=None) == INVALID
     assert call(sb=FAKE + 4) == ALIGN and call(bias=FAKE + 8) == ALIGN
     assert call(M=0, A=None, sa=None, D=None) == OK
