@@ -105,8 +105,11 @@ __device__ __forceinline__ void act_value_grad(int act, float g, float& a, float
 }
 
 // ---- one operand of a tile -------------------------------------------------
-// Position of 16-byte chunk c of row r inside its 128 bytes is c ^ tile_swz(r).
-__device__ __forceinline__ constexpr int tile_swz(int r) { return (r ^ ((r >> 3) & 1)) & 7; }
+// Position of 16-byte chunk c of row r inside its 128 bytes is c ^ tile_swz(r).  A
+// fragment's read (row lane % 16, chunk lane / 16) is served 16 lanes at a time,
+// lanes 0-3, 12-15 and 20-27 first, 4-11, 16-19 and 28-31 next: with r % 8 each of these
+// sixteen meets other banks (no conflicts counted; r ^ r / 8 % 2 doubled every read).
+__device__ __forceinline__ constexpr int tile_swz(int r) { return r & 7; }
 
 // Transposed: 32-byte unit u (16 values) of k row k is kept at u ^ tile_tswz(k).  A
 // transposing read takes, for each 16 lanes, one unit of four consecutive k rows;
@@ -362,20 +365,36 @@ __global__ void __launch_bounds__(64 * WGM * WGN, (tile_waves_simd<BM, BN, RING,
     if (j < decltype(la)::kLoads) la.issue(j, st, rsa, slot);
     else lb.issue(j - decltype(la)::kLoads, st, rsb, slot + kStageA);
   };
-  // `flying`: stages after the next one whose loads may still be under way
+  // `flying`: loads, after those of the next stage, that may still be under way
   auto arrive = [&](auto flying) {
     // this wave's loads of the next stage and its last reads of this one
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(decltype(flying)::value * kIssues) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(decltype(flying)::value) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
+  // Position of the barrier among a stage's MFMAs, and of the loads after it: the memory
+  // pipeline takes 1 KB in 17 clocks, so they are spread over most of a stage's time
+  // and reach into the next stage's MFMAs (kNow of them do not); with two slots over
+  // half of it, for they have to land within that stage.  Loads right behind the
+  // barrier held the MFMAs up: bf16 777 x 4096 x 4096 on 256 x 256 tiles 79 -> 67 us, on
+  // 128 x 128 34 -> 32 with these positions and tile_swz.
+  constexpr int kStageMfma = kGroups * kMfma;
+  constexpr int kBarrier = (kGroups - 2) * kMfma + (kMfma > 1 ? kMfma * 3 / 4 - 1 : 0);
+  constexpr int kSpread = kStageMfma * (RING == 2 ? 8 : 15) / 16 - 1;
+  constexpr int kNow = [] {
+    int n = 0;
+    while (n < kIssues && kBarrier + 1 + n * kSpread / kIssues < kStageMfma) n++;
+    return n;
+  }();
+  static_assert(kBarrier + 1 + (kIssues - 1) * kSpread / kIssues - kStageMfma < kBarrier / kMfma * kMfma,
+                "a stage's loads are issued before the next one's begin");
   // kLeft: stages that follow (RING: that many or more, so stage st + RING is issued)
   auto group = [&](auto left_c, int grp, int st, int slot) {
     constexpr int kLeft = decltype(left_c)::value;
     constexpr bool kNext = kLeft > 0, kAfter = kLeft >= RING;
     const int kk = grp / kParts, part = grp % kParts;
     const bool last = grp == kGroups - 1;
-    if (kAfter && last) begin_issue(st + RING);
+    if (kAfter && grp == kBarrier / kMfma) begin_issue(st + RING);
 #pragma unroll
     for (int t = 0; t < kMfma; t++) {
       const int i = t / TN, j = t % TN;
@@ -387,12 +406,14 @@ __global__ void __launch_bounds__(64 * WGM * WGN, (tile_waves_simd<BM, BN, RING,
         for (int r = 0; r < kReads; r++)
           if (r * (kMfma / 2) / kReads == t) read_one(r, !last ? slot : slot + 1 == RING ? 0 : slot + 1, (grp + 1) % kGroups);
       }
-      if (kNext && grp == kGroups - 2 && t == (kMfma > 1 ? kMfma * 3 / 4 - 1 : 0))
-        arrive(std::integral_constant<int, kLeft < RING ? kLeft - 1 : RING - 2>{});
-      if (kAfter && last) {
+      const int q = grp * kMfma + t;
+      if (kNext && q == kBarrier) arrive(std::integral_constant<int, (kLeft < RING ? kLeft - 1 : RING - 2) * kIssues>{});
 #pragma unroll
-        for (int l = 0; l < kIssues; l++)
-          if (l * kMfma / kIssues == t) issue_one(l, st + RING, slot);
+      for (int l = 0; l < kIssues; l++) {
+        const int at = kBarrier + 1 + l * kSpread / kIssues;
+        if (kAfter && at == q) issue_one(l, st + RING, slot);
+        // what is left of the stage before's
+        if (kLeft >= RING - 1 && at - kStageMfma == q) issue_one(l, st - 1 + RING, slot == 0 ? RING - 1 : slot - 1);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -408,10 +429,10 @@ __global__ void __launch_bounds__(64 * WGM * WGN, (tile_waves_simd<BM, BN, RING,
       if (r < nst) {
         begin_issue(s0 + r);
 #pragma unroll
-        for (int l = 0; l < kIssues; l++) issue_one(l, s0 + r, r);
+        for (int l = 0; l < (r == RING - 1 ? kNow : kIssues); l++) issue_one(l, s0 + r, r);
       }
     // the first stage has landed when the loads after it are all that is out
-    if (nst >= RING) arrive(std::integral_constant<int, RING - 1>{});
+    if (nst >= RING) arrive(std::integral_constant<int, (RING - 2) * kIssues + kNow>{});
     else arrive(std::integral_constant<int, 0>{});
 #pragma unroll
     for (int r = 0; r < kReads; r++) read_one(r, 0, 0);
