@@ -648,15 +648,15 @@ struct TilePlan {
 // compute unit, its start and end round_us; a split's second kernel costs kSplitUs
 // and its partials their bytes.  The figures are a least-squares fit to 2034 timed
 // (shape, kernel, split) combinations, M 48 .. 4096, weights of 1536 x 2048 .. 14336 x
-// 4096, bf16 and int8 (9 % rms); the plan's choice is 0.9 % slower than the best of
-// each shape on average, 12 % at worst.  N counts weight rows (gated: both halves).
+// 4096, bf16 and int8 (9 % rms); the plan's choice is 0.4 % slower than the best of
+// each shape on average, 8 % at worst.  N counts weight rows (gated: both halves).
 struct TileCost {
   int bm, bn, per_cu;
   double us[2], round_us;
 };
-constexpr TileCost kTileCosts[kTileKinds] = {{256, 256, 1, {1.10, 0}, 4.7},  {256, 128, 1, {0.677, 0}, 3.6},
-                                             {128, 128, 2, {0.59, 0.786}, 2.4}, {128, 128, 1, {0.474, 0}, 3.2},
-                                             {64, 128, 2, {0.308, 0.547}, 3.1}, {64, 64, 2, {0.226, 0.357}, 2.8}};
+constexpr TileCost kTileCosts[kTileKinds] = {{256, 256, 1, {1.03, 0}, 4.1},  {256, 128, 1, {0.62, 0}, 3.0},
+                                             {128, 128, 2, {0.542, 0.767}, 2.1}, {128, 128, 1, {0.423, 0}, 2.7},
+                                             {64, 128, 2, {0.279, 0.533}, 2.6}, {64, 64, 2, {0.214, 0.342}, 2.3}};
 
 // Estimated time of `items` workgroups of `stages` stages each.
 inline double tile_time(const TileCost& c, int64_t items, double stages, int cus) {
@@ -665,7 +665,7 @@ inline double tile_time(const TileCost& c, int64_t items, double stages, int cus
 }
 
 inline TilePlan plan_tile(int64_t M, int64_t N, int64_t kbytes, int cus) {
-  constexpr double kSplitUs = 3.3, kPartBytesUs = 5.0e6;
+  constexpr double kSplitUs = 3.8, kPartBytesUs = 5.0e6;
   const int64_t stages = (kbytes + kTileStage - 1) / kTileStage;
   auto tiles = [](const TileCost& c, int64_t m, int64_t n) { return ((m + c.bm - 1) / c.bm) * ((n + c.bn - 1) / c.bn); };
   TilePlan best{kTile256, 1, 0, 0, kTile256};

@@ -10,14 +10,16 @@ from test_gpu_gated_ffn import backward_reference, problem, sum_error
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 
-#: rows, weight rows (gated: both halves), bytes of a row: the smallest of its kind each
+#: rows, weight rows (gated: both halves), bytes of a row
 SHAPES = {
-    "128": (336, 6160, 288), "128 cols+64": (608, 14352, 2080), "128 rows+64": (2064, 4112, 2080),
-    "128 split": (336, 6160, 8224), "deep": (336, 6160, 2080), "deep split": (80, 6160, 8224),
-    "256": (5008, 6160, 288), "256 cols+deep": (2512, 14352, 2080), "256 cols+256x128": (5008, 14352, 2080),
-    "256 cols+64": (4096, 4112, 2080), "256 rows+256x128": (5008, 4112, 8224), "256 rows+64": (2064, 14352, 2080),
-    "256x128": (2064, 14352, 288), "256x128 rows+64": (5008, 1552, 2080), "256x128 rows+64x128": (2064, 4112, 8224),
-    "256x128 split": (208, 10256, 8224), "64": (80, 272, 288), "64 split": (80, 272, 8224), "64x128": (80, 10256, 2080),
+    "128": (336, 6160, 288), "128 cols+64": (80, 68768, 1472), "128 cols+64x128": (80, 79056, 1216),
+    "128 rows+64": (2064, 4336, 1024), "128 split": (80, 11024, 11040), "deep": (336, 6160, 2080),
+    "deep split": (80, 6160, 8224), "256": (5008, 6160, 288), "256 cols+deep": (2512, 14352, 2080),
+    "256 cols+256x128": (5008, 14352, 2080), "256 cols+128": (640, 34320, 1280), "256 cols+64": (4096, 4112, 2080),
+    "256 rows+256x128": (5008, 4112, 8224), "256 rows+128": (640, 95120, 320), "256 rows+64": (2064, 14352, 2080),
+    "256 split": (144, 12000, 12704), "256x128": (2064, 14352, 288), "256x128 cols+64": (208, 33744, 928),
+    "256x128 rows+64": (5008, 1552, 2080), "256x128 rows+64x128": (2064, 4112, 8224),
+    "256x128 split": (144, 5568, 9216), "64": (80, 272, 288), "64 split": (80, 272, 8224), "64x128": (80, 10256, 2080),
     "64x128 split": (80, 2064, 8224),
 }
 
