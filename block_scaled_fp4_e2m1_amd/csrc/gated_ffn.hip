@@ -47,16 +47,58 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+// Both products of a small layer in one launch: the workgroups of one fill the units
+// that the other leaves free.  The product of longer sums goes first.
+__global__ void __launch_bounds__(256, (tile_waves_simd<64, 128, 3, 4>()))
+    gated_products(const TileArgs dx, const TileArgs dw, int dw_first) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[tile_smem<64, 128, 3>()];
+  const int n_dx = dx.tiles_m * dx.tiles_n, n_dw = dw.tiles_m * dw.tiles_n;
+  const int lead = dw_first ? n_dw : n_dx;
+  const bool first = (int)blockIdx.x < lead;
+  const int block = first ? blockIdx.x : blockIdx.x - lead;
+  if (first == (dw_first != 0)) tile_body<false, 64, 128, 2, 2, 3, true, true, kTileStore>(dw, block, smem);
+  else tile_body<false, 64, 128, 2, 2, 3, false, true, kTileStore>(dx, block, smem);
+}
+
 struct BwdPlan {
   TilePlan dx, dw;
+  bool joint;        // both in one launch of gated_products
   size_t dgu, part;  // workspace bytes of [dG | dU] and of the larger product's partials
 };
+
+// One launch where each of the 64 x 128 tile's slots (two per unit) has no more K stages
+// than this to do.  Whole backward passes, one launch against two: 256 x 4096 x 1024 (M,
+// H, I; 16 stages) 20.9 us against 25.0, 777 x 2048 x 776 (20) 27.6 against 29.4, 4096 x
+// 512 x 1024 (32) 39.2 against 43.4, 1024 x 2048 x 1536 (48) 42.3 against 44.6; beyond,
+// larger tiles win: 1500 x 3000 x 1000 (72) 69.6 against 59.7.  Only where neither
+// product alone is split over K, so that a gradient's bits do not depend on whether the
+// other one is asked for.
+constexpr int64_t kJointStages = 48;
+
+int64_t joint_tiles(int64_t m, int64_t n) {
+  const TileCost& c = kTileCosts[kTile64x128];
+  return (m + c.bm - 1) / c.bm * ((n + c.bn - 1) / c.bn);
+}
+
+hipError_t launch_products(TileArgs dx, TileArgs dw, hipStream_t stream) {
+  for (TileArgs* a : {&dx, &dw}) {
+    a->tiles_m = (a->M + 63) / 64;
+    a->tiles_n = (a->N + 127) / 128;
+    a->splits = 1;
+  }
+  const unsigned grid = (unsigned)(dx.tiles_m * dx.tiles_n + dw.tiles_m * dw.tiles_n);
+  gated_products<<<grid, 256, 0, stream>>>(dx, dw, dw.kend > dx.kend);
+  return hipGetLastError();
+}
 
 BwdPlan plan_bwd(int64_t M, int64_t H, int64_t I) {
   const int cus = device_cu_count();
   BwdPlan b;
   b.dx = plan_tile(M, H, 4 * I, cus);
   b.dw = plan_tile(2 * I, H, 2 * M, cus);
+  const int64_t stages = joint_tiles(M, H) * ((4 * I + kTileStage - 1) / kTileStage) +
+                         joint_tiles(2 * I, H) * ((2 * M + kTileStage - 1) / kTileStage);
+  b.joint = b.dx.splits == 1 && b.dw.splits == 1 && stages <= kJointStages * 2 * cus;
   b.dgu = ((size_t)M * 2 * I * 2 + 255) / 256 * 256;
   b.part = std::max(tile_workspace(b.dx, M, H), tile_workspace(b.dw, 2 * I, H));
   return b;
@@ -104,32 +146,23 @@ hipError_t launch_gated_ffn_bwd(const uint16_t* dh, const uint16_t* x, const uin
                                                                                            (int)I, dgu);
     e = hipGetLastError();
   }
-  if (e == hipSuccess && dx != nullptr) {
-    TileArgs a{};
-    a.A = reinterpret_cast<const uint8_t*>(dgu);
-    a.lda = 4 * I;
-    a.B = reinterpret_cast<const uint8_t*>(W);
-    a.ldb = 2 * H;
-    a.M = (int)M;
-    a.N = (int)H;
-    a.kend = 2 * I;  // k rows of W
-    a.D = dx;
-    a.part = part;
-    e = launch_tile<false, false, true, kTileStore>(a, b.dx, stream);
-  }
-  if (e == hipSuccess && dW != nullptr) {
-    TileArgs a{};
-    a.A = reinterpret_cast<const uint8_t*>(dgu);
-    a.lda = 4 * I;
-    a.B = reinterpret_cast<const uint8_t*>(x);
-    a.ldb = 2 * H;
-    a.M = (int)(2 * I);
-    a.N = (int)H;
-    a.kend = M;  // k rows of dgu and x
-    a.D = dW;
-    a.part = part;
-    e = launch_tile<false, true, true, kTileStore>(a, b.dw, stream);
-  }
+  TileArgs ax{}, aw{};
+  ax.A = aw.A = reinterpret_cast<const uint8_t*>(dgu);
+  ax.lda = aw.lda = 4 * I;
+  ax.B = reinterpret_cast<const uint8_t*>(W);
+  aw.B = reinterpret_cast<const uint8_t*>(x);
+  ax.ldb = aw.ldb = 2 * H;
+  ax.M = (int)M;
+  aw.M = (int)(2 * I);
+  ax.N = aw.N = (int)H;
+  ax.kend = 2 * I;  // k rows of W
+  aw.kend = M;      // k rows of dgu and x
+  ax.D = dx;
+  aw.D = dW;
+  ax.part = aw.part = part;
+  if (e == hipSuccess && dx != nullptr && dW != nullptr && b.joint) return launch_products(ax, aw, stream);
+  if (e == hipSuccess && dx != nullptr) e = launch_tile<false, false, true, kTileStore>(ax, b.dx, stream);
+  if (e == hipSuccess && dW != nullptr) e = launch_tile<false, true, true, kTileStore>(aw, b.dw, stream);
   return e;
 }
 

@@ -272,11 +272,10 @@ constexpr int tile_waves_simd() {
 // Work item of a workgroup.  Workgroups are dispatched round-robin over the 8
 // XCDs; consecutive items go to one XCD and run down bands of `band` tile rows, so
 // an XCD's items share few A and B panels in its L2.
-__device__ __forceinline__ void tile_item(const TileArgs& p, int& tile_m, int& tile_n, int& split) {
+__device__ __forceinline__ void tile_item(const TileArgs& p, int item, int& tile_m, int& tile_n, int& split) {
   const int items = p.tiles_m * p.tiles_n * p.splits;
   // the first 8 * (items / 8) workgroups are remapped, the rest keep their index
   const int per = items / 8;
-  int item = blockIdx.x;
   if (item < per * 8) item = (item % 8) * per + item / 8;
   split = item % p.splits;
   const int tile = item / p.splits;
@@ -288,9 +287,9 @@ __device__ __forceinline__ void tile_item(const TileArgs& p, int& tile_m, int& t
   tile_n = in_band / rows;
 }
 
+// Work item `block` of p, in tile_smem bytes of LDS.
 template <bool kInt8, int BM, int BN, int WGM, int WGN, int RING, bool kTransA, bool kTransB, int EPI>
-__global__ void __launch_bounds__(64 * WGM * WGN, (tile_waves_simd<BM, BN, RING, WGM * WGN>()))
-    tile_gemm(const TileArgs p) {
+__device__ __forceinline__ void tile_body(const TileArgs& p, int block, uint8_t* smem) {
   typedef Mma<kInt8> MM;
   constexpr int NT = 64 * WGM * WGN, WAVES = WGM * WGN;
   constexpr int WM = BM / WGM, WN = BN / WGN, TM = WM / 16, TN = WN / 16;
@@ -299,12 +298,11 @@ __global__ void __launch_bounds__(64 * WGM * WGN, (tile_waves_simd<BM, BN, RING,
   static_assert(RING >= 2 && RING <= 4, "ring depth");
   static_assert(!kGated || TN % 2 == 0, "a wave holds pairs of gate and up blocks");
   static_assert(!kInt8 || (!kTransA && !kTransB), "8-bit operands have their rows along K");
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[tile_smem<BM, BN, RING>()];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WGN, wn = wave % WGN, kg = lane >> 4, lr = lane & 15;
   int tile_m, tile_n, split;
-  tile_item(p, tile_m, tile_n, split);
+  tile_item(p, block, tile_m, tile_n, split);
   constexpr int kCols = kGated ? BN / 2 : BN;  // output columns of a tile
   const int m0 = p.m_base + tile_m * BM, n0 = p.n_base + tile_n * kCols;
 
@@ -575,6 +573,13 @@ __global__ void __launch_bounds__(64 * WGM * WGN, (tile_waves_simd<BM, BN, RING,
   }
 }
 
+template <bool kInt8, int BM, int BN, int WGM, int WGN, int RING, bool kTransA, bool kTransB, int EPI>
+__global__ void __launch_bounds__(64 * WGM * WGN, (tile_waves_simd<BM, BN, RING, WGM * WGN>()))
+    tile_gemm(const TileArgs p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[tile_smem<BM, BN, RING>()];
+  tile_body<kInt8, BM, BN, WGM, WGN, RING, kTransA, kTransB, EPI>(p, blockIdx.x, smem);
+}
+
 // ---- split K ---------------------------------------------------------------
 // Sums the splits' partials in split order (8-bit: exact integers) and finishes
 // the rows as the tile's epilogue would.  One thread: eight output columns.
@@ -641,6 +646,7 @@ struct TilePlan {
   // from `cut` on are a second launch of kernel `rest`.  0: everything in one.
   int64_t cut_m, cut_n;
   TileKind rest;
+  double us;  // the estimate
 };
 
 // Kernel and K split of an M x N (x K bytes) product: the choice with the least
@@ -668,13 +674,9 @@ inline TilePlan plan_tile(int64_t M, int64_t N, int64_t kbytes, int cus) {
   constexpr double kSplitUs = 3.8, kPartBytesUs = 5.0e6;
   const int64_t stages = (kbytes + kTileStage - 1) / kTileStage;
   auto tiles = [](const TileCost& c, int64_t m, int64_t n) { return ((m + c.bm - 1) / c.bm) * ((n + c.bn - 1) / c.bn); };
-  TilePlan best{kTile256, 1, 0, 0, kTile256};
-  double best_t = 1e300;
-  auto consider = [&](double t, const TilePlan& pl) {
-    if (t < best_t * 0.999) {
-      best_t = t;
-      best = pl;
-    }
+  TilePlan best{kTile256, 1, 0, 0, kTile256, 1e300};
+  auto consider = [&](const TilePlan& pl) {
+    if (pl.us < best.us * 0.999) best = pl;
   };
   for (int c = 0; c < kTileKinds; c++) {
     const TileCost& cd = kTileCosts[c];
@@ -683,7 +685,7 @@ inline TilePlan plan_tile(int64_t M, int64_t N, int64_t kbytes, int cus) {
       if (sp > 1 && (stages / sp < 4 || all * (sp - 1) >= slots)) break;
       double t = tile_time(cd, all * sp, (double)((stages + sp - 1) / sp), cus);
       if (sp > 1) t += kSplitUs + 2.0 * sp * M * N * 4 / kPartBytesUs;
-      consider(t, TilePlan{(TileKind)c, sp, 0, 0, kTile256});
+      consider(TilePlan{(TileKind)c, sp, 0, 0, kTile256, t});
     }
     // a part-filled last round (896 tiles of 256 x 256 on 256 units: 3.5 rounds) goes
     // to smaller tiles: bf16 gated with its sums kept, 4096 x 14336 x 4096, 420 -> 397
@@ -699,8 +701,8 @@ inline TilePlan plan_tile(int64_t M, int64_t N, int64_t kbytes, int cus) {
       for (int r = 0; r < kTileKinds; r++) {
         const TileCost& rd = kTileCosts[r];
         const int64_t left = dir ? tiles(rd, M, N - cut) : tiles(rd, M - cut, N);
-        consider(t_main + tile_time(rd, left, (double)stages, cus),
-                 TilePlan{(TileKind)c, 1, dir ? 0 : cut, dir ? cut : 0, (TileKind)r});
+        consider(TilePlan{(TileKind)c, 1, dir ? 0 : cut, dir ? cut : 0, (TileKind)r,
+                          t_main + tile_time(rd, left, (double)stages, cus)});
       }
     }
   }

@@ -64,7 +64,7 @@ def backward_reference(dh, x, W, gate_up, act):
 
 @pytest.mark.parametrize("M,H,I", [(1, 8, 8), (3, 72, 40), (15, 256, 128), (63, 264, 72), (64, 512, 256),
                                    (65, 1032, 264), (200, 2048, 776), (513, 520, 1544), (777, 2048, 768),
-                                   (1024, 1024, 1024)])
+                                   (1024, 1024, 1024), (256, 4096, 1024), (4096, 512, 1024), (1500, 2056, 1000)])
 @pytest.mark.parametrize("act", ACTS)
 def test_backward(M, H, I, act):
     x, W, dh = problem(M, H, I, seed=1)
