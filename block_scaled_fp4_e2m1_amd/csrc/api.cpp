@@ -337,6 +337,15 @@ bsfp4_status check_act(int act) {
   return BSFP4_OK;
 }
 
+// A launch holds fewer than 2^32 threads; the row kernels have at most four times one
+// per eight values, 64 at least.
+bsfp4_status check_row_count(int64_t rows, int64_t cols) {
+  if (rows >= (int64_t)1 << 26 || rows * cols >= (int64_t)1 << 33)
+    return fail(BSFP4_ERR_SHAPE, "%lld rows of %lld: need fewer than 2^26 rows and 2^33 values in a call",
+                (long long)rows, (long long)cols);
+  return BSFP4_OK;
+}
+
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
@@ -345,7 +354,8 @@ bsfp4_status bsfp4_int8_quantize(const uint16_t* x, int64_t M, int64_t K, int8_t
   if (M < 0 || K <= 0)
     return fail(BSFP4_ERR_SHAPE, "need M >= 0 and K > 0 (M=%lld K=%lld)", (long long)M, (long long)K);
   if (K % 8) return fail(BSFP4_ERR_SHAPE, "K=%lld is not a multiple of 8", (long long)K);
-  if (M > INT32_MAX || K > INT32_MAX) return fail(BSFP4_ERR_SHAPE, "dimensions must fit in 31 bits");
+  if (K > INT32_MAX) return fail(BSFP4_ERR_SHAPE, "dimensions must fit in 31 bits");
+  if (bsfp4_status e = check_row_count(M, K)) return e;
   if (M == 0) return ok();
   REQUIRE_PTR(x);
   REQUIRE_PTR(q);
@@ -388,6 +398,7 @@ bsfp4_status bsfp4_int8_quantize_gemm(const uint16_t* x, const int8_t* B, const 
                                       void* stream) {
   if (bsfp4_status e = check_rows_cols("M", M, "N", N, 8, "K", K, 16)) return e;
   if (bsfp4_status e = check_int8_k(K)) return e;
+  if (bsfp4_status e = check_row_count(M, K)) return e;
   if (M > 0) {
     REQUIRE_PTR(x);
     REQUIRE_PTR(D);
@@ -504,7 +515,8 @@ bsfp4_status check_block_norm(const bsfp4_block_norm_args* a) {
   if (a->H % 8) return fail(BSFP4_ERR_SHAPE, "H=%lld is not a multiple of 8", (long long)a->H);
   if (a->H > bsfp4::kBlockNormMaxH)
     return fail(BSFP4_ERR_SHAPE, "H=%lld exceeds %lld", (long long)a->H, (long long)bsfp4::kBlockNormMaxH);
-  if (a->T > INT32_MAX || a->groups > INT32_MAX) return fail(BSFP4_ERR_SHAPE, "dimensions must fit in 31 bits");
+  if (bsfp4_status e = check_row_count(a->T, a->H)) return e;
+  if (a->groups > INT32_MAX) return fail(BSFP4_ERR_SHAPE, "dimensions must fit in 31 bits");
   if (a->T % a->groups)
     return fail(BSFP4_ERR_SHAPE, "T=%lld is not a multiple of groups=%lld", (long long)a->T, (long long)a->groups);
   if (!(a->eps > 0.0 && a->eps < 1e30)) return fail(BSFP4_ERR_INVALID_ARG, "eps must be positive and finite");

@@ -403,7 +403,7 @@ BSFP4_API bsfp4_status nvfp4_moe_grouped_gemm(const uint8_t* Aq, const uint8_t* 
  *   A row of zeros gives s = 0 and q = 0.  A row with an infinity or a NaN
  *   gives s = NaN and q = 0, so every result computed from it is NaN.
  *   x    device bf16 [M, K], M >= 0, K > 0, K % 8 == 0 (the products below
- *        take K % 16 == 0)
+ *        take K % 16 == 0), M < 2^26, M K < 2^33
  *   q    device int8 [M, K]
  *   s    device float [M]
  *
@@ -420,7 +420,7 @@ BSFP4_API bsfp4_status nvfp4_moe_grouped_gemm(const uint8_t* Aq, const uint8_t* 
  *            (may be NULL when that is 0); needs no initialisation
  *
  * bsfp4_int8_quantize_gemm: bsfp4_int8_gemm(bsfp4_int8_quantize(x), B) in one
- *   call, bit for bit the output of the two.
+ *   call, bit for bit the output of the two (sizes of both).
  *   ws       bsfp4_int8_quantize_gemm_workspace_size(M, N, K) bytes
  *
  * bsfp4_int8_gated_ffn: h[M,I] = bf16_rne(act(G) * U) with [G | U] the scaled
@@ -499,7 +499,8 @@ BSFP4_API bsfp4_status bsfp4_gated_ffn_backward(const uint16_t* dh, const uint16
  *   res_out    bf16 [T, H]; may be `residual` or `x` itself
  *   z          bf16 [T, H]; or NULL and, instead of it,
  *   q, s       int8 [T, H], float [T]: bsfp4_int8_quantize of z
- *   sizes      T >= 0, H > 0, H % 8 == 0, H <= 16384, groups >= 1, eps > 0
+ *   sizes      T >= 0, H > 0, H % 8 == 0, H <= 16384, T < 2^26, T H < 2^33,
+ *              groups >= 1, eps > 0
  *
  * bsfp4_block_norm_backward: gradients of the above (z in bf16) from dres_out
  *   and dz.  Row sums and the vectors' gradients are FP32 or wider; the

@@ -131,6 +131,7 @@ def test_abi_int8(lib):
     assert f(FAKE + 8, 2, 16, FAKE, FAKE, None) == ALIGN
     assert f(FAKE, 2, 16, FAKE, FAKE + 2, None) == ALIGN
     assert f(None, 0, 16, None, None, None) == OK
+    assert f(FAKE, 1 << 26, 16, FAKE, FAKE, None) == SHAPE and f(FAKE, 1 << 25, 256, FAKE, FAKE, None) == SHAPE
     g = lib.bsfp4_int8_gemm
 
     def call(A=FAKE, sa=FAKE, B=FAKE, sb=FAKE, bias=None, D=FAKE, M=2, N=64, K=64, ws=None, n=0):
@@ -185,6 +186,7 @@ def test_abi_block_norm(lib):
 
     assert lib.bsfp4_block_norm(None, None) == INVALID
     assert call(H=60) == SHAPE and call(H=16392) == SHAPE and call(T=-1) == SHAPE and call(groups=0) == SHAPE
+    assert call(T=1 << 26) == SHAPE and call(T=1 << 20, H=8192) == SHAPE and "2^33" in err(lib)
     assert call(x=FAKE, res_out=FAKE, gate=FAKE, groups=3) == SHAPE
     assert call(x=FAKE, res_out=FAKE, groups=2) == SHAPE and "without a gate" in err(lib)
     assert call(x=FAKE, res_out=FAKE, eps=0.0) == INVALID
