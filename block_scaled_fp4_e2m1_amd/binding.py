@@ -190,7 +190,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(device) -> ctypes.c_void_p:
-    if _raw_stream is not None and device.index is not None:
+    if _raw_stream is not None and isinstance(device, torch.device) and device.index is not None:
         return ctypes.c_void_p(_raw_stream(device.index))
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 

@@ -70,6 +70,16 @@ def test_norm_feeds_the_fp4_quantiser(fmt):
         assert torch.equal(a, c)
 
 
+@pytest.mark.parametrize("device", [0, "cuda", "cuda:0", torch.device("cuda"), torch.device("cuda:0")], ids=repr)
+def test_current_stream_of_any_device_form(device):
+    """The binding's stream handle, for whatever names a device."""
+    from block_scaled_fp4_e2m1_amd import binding
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        assert binding._stream(device).value == side.cuda_stream
+    assert (binding._stream(device).value or 0) == torch.cuda.current_stream().cuda_stream
+
+
 def test_other_streams_and_two_at_once():
     b1, b2 = Block(64, 1024, 512, 1), Block(130, 512, 784, 2)
     want1, want2 = b1.serve(), b2.serve()
