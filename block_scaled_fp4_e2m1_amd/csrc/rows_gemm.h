@@ -15,6 +15,11 @@
 // and chunks past K are zeros through the buffers' range check.  The waves' sums are
 // added in wave order by one wave, which finishes the outputs.
 //
+// Bound by the weight's bytes from some 20 MB on: bf16 gated 1 x 14336 x 4096 (117 MB)
+// 20.7 us, 5.7 TB/s out of the memory-side cache, 41 us from HBM behind dirty lines; int8
+// 8 x 65536 x 4096 (268 MB) 48 us, 5.6 TB/s.  Smaller ones are a launch and two memory
+// latencies (int8 16 x 1024 x 4096 3.5 us).
+//
 // kQuant (8-bit): the activations come in bf16 and every workgroup quantises all of
 // them into LDS itself, its first weight loads already under way: one launch and no
 // intermediate for a token's projection.
@@ -233,15 +238,19 @@ hipError_t launch_rows(const TileArgs& a, hipStream_t stream) {
 
 // Whether a product of M rows with n weight rows (gated: both halves) of kbytes runs
 // on rows_gemm.  Every workgroup reads all activation rows, so past some M n the tiles
-// are faster: int8 16 x 4096 x 14336 10.7 us against 11.0, 32 x 4096 x 14336 11.9
-// against 11.2; 32 x 4096 x 8192 7.3 against 9.8; 64 x 7168 x 4096 9.0 against 10.8.
-// Few rows keep it longer, where K has steps enough for the waves' rings (8 turns or
-// more of 128 bytes each): int8 8 x 131072 x 4096 96 against 114, 16 x 65536 x 4096 53
-// against 62, bf16 gated 1 x 32768 x 4096 48 against 61; but bf16 gated 16 x 131072 x
-// 4096 196 against 176, int8 4 x 131072 x 1024 35 against 27.
+// are faster: int8 32 x 4096 x 14336 10.8 us against 14.8, 64 x 4096 x 4096 6.2 against
+// 8.9, but 64 x 7168 x 4096 9.9 against 9.1.  Few rows keep it longer, where K has steps
+// enough for the waves' rings (4096 bytes): int8 8 x 131072 x 4096 96 against 117, 16 x
+// 65536 x 4096 53 against 63, bf16 gated 1 x 32768 x 4096 49 against 63; but bf16 gated
+// 16 x 131072 x 4096 194 against 175, int8 4 x 131072 x 1024 35 against 27.
+// And past some M kbytes the activations are most of what a workgroup reads, where the
+// tiles split K: bf16 gated 32 x 4096 x 14336 29 against 27, 64 x 4096 x 14336 40 against
+// 29, 48 x 1024 x 14336 22 against 18; 32 x 2048 x 14336 17 against 21, int8 48 x 4096 x
+// 14336 13.4 against 15.9.
 inline bool rows_ok(int64_t M, int64_t n, int64_t kbytes) {
   const bool few = M <= 16 && kbytes >= 4096;
-  return M <= kRowsMaxM && M * n <= ((int64_t)1 << (few ? 20 : 18));
+  return M <= kRowsMaxM && M * n <= ((int64_t)1 << (few ? 20 : 18)) &&
+         M * kbytes <= (M <= 32 ? (int64_t)4 << 18 : (int64_t)3 << 18);
 }
 
 // 8-bit, the activations x in bf16 (a.M <= 4, whole 128-byte steps of codes within

