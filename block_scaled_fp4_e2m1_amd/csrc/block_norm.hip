@@ -171,8 +171,11 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT)
 template <int NT, int CH, bool kAll>
 __global__ void __launch_bounds__(NT, 4)
     block_norm_bwd(const BlockNormArgs p) {
-  __shared__ double red_a[3 * (NT / 64)];
+  // with w_post the second reduction's barrier stands between a row's reads of red_a and
+  // the next row's writes; without, red_a alternates row by row
+  __shared__ double red_a[kAll ? 1 : 2][3 * (NT / 64)];
   __shared__ double red_b[NT / 64];
+  int parity = 0;
   const int t = threadIdx.x;
   const int H = p.H, chunks = H / 8;
   const bool has_x = kAll || p.x != nullptr, has_post = kAll || p.w_post != nullptr, has_pre = kAll || p.w_pre != nullptr,
@@ -252,7 +255,8 @@ __global__ void __launch_bounds__(NT, 4)
         }
       }
       __builtin_amdgcn_sched_barrier(0);
-      row_sum<NT>(s, red_a);
+      row_sum<NT>(s, red_a[parity]);
+      if (!kAll) parity ^= 1;
       __builtin_amdgcn_sched_barrier(0);
       const float xs = has_x && has_post ? rstd_of(s[0], p.inv_h, p.eps) : 1.0f;
       const float rs = has_pre ? rstd_of(s[1], p.inv_h, p.eps) : 1.0f;

@@ -163,6 +163,24 @@ def test_backward(T, H, groups, parts):
     assert all(got[n] is None or torch.equal(got[n], again[n]) for n in names)
 
 
+@pytest.mark.parametrize("T,H", [(6000, 8192), (9000, 2048)])
+@pytest.mark.parametrize("parts", ["no_post", "pre_only"])
+def test_backward_long_strips_without_post_norm(T, H, parts):
+    """Many rows per workgroup with one reduction each: every row's sums are its own, the first time and again."""
+    p, dres, dz = problem(T, H, 1, seed=11)
+    p["w_post"] = None
+    if parts == "pre_only":
+        p["x"] = p["gate"] = None
+    kw = dict(w_post=None, w_pre=p["w_pre"], gate=p["gate"], scale=0.3, eps=EPS)
+    res, _ = bs.block_norm(p["x"], p["residual"], **kw)
+    got = bs.block_norm_backward(dres, dz, p["x"], res, **kw)
+    ref, mag = reference_backward(dres, dz, p, res, 0.3)["dres"]
+    R.check(got[1], ref, 64 * R.F32 * mag, parts)
+    for _ in range(3):
+        again = bs.block_norm_backward(dres, dz, p["x"], res, **kw)
+        assert all(a is None or torch.equal(a, b) for a, b in zip(got, again))
+
+
 def test_backward_against_differences():
     """L = sum(dres res) + sum(dz z) as a 64-bit function of every input (res unrounded), central differences along
     random directions.  The kernel takes the gradient at the stored (rounded) res: 2^-8 of it, averaged."""
