@@ -346,6 +346,12 @@ bsfp4_status check_row_count(int64_t rows, int64_t cols) {
   return BSFP4_OK;
 }
 
+// An output that shares memory with an input other workgroups still read.
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+  return a != nullptr && b != nullptr && pa < pb + (uintptr_t)nb && pb < pa + (uintptr_t)na;
+}
+
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
@@ -408,6 +414,7 @@ bsfp4_status bsfp4_int8_quantize_gemm(const uint16_t* x, const int8_t* B, const 
   if (bias != nullptr && !aligned(bias, 16)) return fail(BSFP4_ERR_ALIGNMENT, "bias is not 16-byte aligned");
   if (bsfp4_status e = check_workspace(ws, ws_bytes, bsfp4_int8_quantize_gemm_workspace_size(M, N, K))) return e;
   if (M == 0) return ok();
+  if (overlap(D, M * N * 2, x, M * K * 2)) return fail(BSFP4_ERR_INVALID_ARG, "D overlaps x");
   if (bsfp4_status e = check_device()) return e;
   if (bsfp4::int8_fused_quant_ok(M, K))
     return launched(bsfp4::launch_int8_fused_quant_gemm(x, B, sb, bias, D, M, N, K, as_stream(stream)),
@@ -472,6 +479,8 @@ bsfp4_status bsfp4_gated_ffn(const uint16_t* x, const uint16_t* W, int act, uint
   if (gate_up != nullptr && !aligned(gate_up, 16)) return fail(BSFP4_ERR_ALIGNMENT, "gate_up is not 16-byte aligned");
   if (bsfp4_status e = check_workspace(ws, ws_bytes, bsfp4_gated_ffn_workspace_size(M, I, H))) return e;
   if (M == 0) return ok();
+  if (overlap(h, M * I * 2, x, M * H * 2) || overlap(h, M * I * 2, W, 4 * I * H))
+    return fail(BSFP4_ERR_INVALID_ARG, "h overlaps x or W");
   if (bsfp4_status e = check_device()) return e;
   return launched(bsfp4::launch_gated_ffn(x, W, act, h, gate_up, M, I, H, ws, as_stream(stream)),
                   "bsfp4_gated_ffn launch");
@@ -571,6 +580,10 @@ bsfp4_status bsfp4_block_norm(const bsfp4_block_norm_args* a, void* stream) {
   if (a->x != nullptr) REQUIRE_FIELD(res_out);
   if (a->w_pre != nullptr && a->z == nullptr && a->q == nullptr)
     return fail(BSFP4_ERR_INVALID_ARG, "w_pre without z or q");
+  const int64_t bytes = 2 * a->T * a->H;
+  for (const uint16_t* in : {a->x, a->residual})
+    if (a->x != nullptr && a->res_out != in && overlap(a->res_out, bytes, in, bytes))
+      return fail(BSFP4_ERR_INVALID_ARG, "res_out overlaps x or residual without being it");
   if (bsfp4_status e = check_device()) return e;
   bsfp4::BlockNormArgs p = norm_args(a);
   p.res_out = a->res_out;

@@ -420,7 +420,7 @@ BSFP4_API bsfp4_status nvfp4_moe_grouped_gemm(const uint8_t* Aq, const uint8_t* 
  *            (may be NULL when that is 0); needs no initialisation
  *
  * bsfp4_int8_quantize_gemm: bsfp4_int8_gemm(bsfp4_int8_quantize(x), B) in one
- *   call, bit for bit the output of the two (sizes of both).
+ *   call, bit for bit the output of the two (sizes of both; D must not overlap x).
  *   ws       bsfp4_int8_quantize_gemm_workspace_size(M, N, K) bytes
  *
  * bsfp4_int8_gated_ffn: h[M,I] = bf16_rne(act(G) * U) with [G | U] the scaled
@@ -458,7 +458,7 @@ BSFP4_API bsfp4_status bsfp4_int8_gated_ffn(const int8_t* A, const float* sa, co
  * bsfp4_gated_ffn: [G | U] = x W^T (FP32 sums), h = bf16_rne(act(G) * U).
  *   x        device bf16 [M, H], M >= 0
  *   W        device bf16 [2 I, H]: gate rows, then up rows
- *   h        device bf16 [M, I]
+ *   h        device bf16 [M, I], not overlapping x or W
  *   gate_up  device float [M, 2 I] or NULL: [G | U] for the backward pass
  *   sizes    H > 0, I > 0, multiples of 8, H < 2^22, I < 2^21
  *   ws       bsfp4_gated_ffn_workspace_size(M, I, H) bytes
@@ -496,7 +496,8 @@ BSFP4_API bsfp4_status bsfp4_gated_ffn_backward(const uint16_t* dh, const uint16
  *   w_post     bf16 [H] or NULL;  w_pre  bf16 [H] or NULL (no z)
  *   gate       bf16 [groups, H] or NULL (1); rows [g T/groups, (g+1) T/groups)
  *              use gate row g; T % groups == 0
- *   res_out    bf16 [T, H]; may be `residual` or `x` itself
+ *   res_out    bf16 [T, H]; may be `residual` or `x` itself, but must not
+ *              overlap them otherwise
  *   z          bf16 [T, H]; or NULL and, instead of it,
  *   q, s       int8 [T, H], float [T]: bsfp4_int8_quantize of z
  *   sizes      T >= 0, H > 0, H % 8 == 0, H <= 16384, T < 2^26, T H < 2^33,

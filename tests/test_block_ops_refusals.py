@@ -206,3 +206,18 @@ def test_abi_block_norm(lib):
         assert call(**{**b, missing: None}) == INVALID, missing
     assert call(**b, gate=FAKE) == INVALID and "dgate" in err(lib)
     assert call(**b, n=16) == WORKSPACE
+
+
+def test_abi_overlapping_outputs(lib):
+    """Outputs that share bytes with an input other workgroups still read."""
+    far = FAKE + (1 << 32)
+    f = lib.bsfp4_int8_quantize_gemm
+    for D in (far, far + 2 * 64 - 16, far - 2 * 64 + 16):
+        assert f(far, FAKE, FAKE, None, D, 1, 64, 64, None, 0, None) == INVALID and "overlaps" in err(lib)
+    f = lib.bsfp4_gated_ffn
+    for x, W, h in ((far, FAKE, far), (FAKE, far, far + 2 * 32 * 64 - 16), (far, FAKE, far + 4 * 64 * 2 - 16)):
+        assert f(x, W, 0, h, None, 4, 16, 64, FAKE, 1 << 30, None) == INVALID and "overlaps" in err(lib)
+    for res_out in (far + 128, far - 128):
+        for kw in (dict(x=far, residual=FAKE), dict(x=FAKE, residual=far)):
+            a = binding.BlockNormArgs(scale=1.0, eps=1e-6, T=4, H=64, groups=1, res_out=res_out, **kw)
+            assert lib.bsfp4_block_norm(ctypes.byref(a), None) == INVALID and "overlaps" in err(lib)

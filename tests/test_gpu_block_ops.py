@@ -131,6 +131,19 @@ def test_graphs(T, H, I):
             assert torch.equal(a, w)
 
 
+def test_overlapping_outputs_are_refused():
+    x = torch.randn((70, 64), device=DEV).to(torch.bfloat16)
+    W = torch.randn((128, 64), device=DEV).to(torch.bfloat16)
+    q, s = bs.int8_quantize(W[:64].contiguous())
+    before = x.clone()
+    for call in (lambda: bs.gated_ffn(x, W, out=x), lambda: bs.int8_quantize_gemm(x, q, s, out=x),
+                 lambda: bs.block_norm(x[:-1], W[:69], res_out=x[1:])):
+        with pytest.raises(bs.Bsfp4Error, match="overlaps"):
+            call()
+    torch.cuda.synchronize()
+    assert torch.equal(x, before)
+
+
 def test_training_chain_against_differences():
     """The whole trained block's gradient with respect to its weight and its input, along random directions, against
     central differences of the 64-bit block (no roundings in between).  Every stage's bf16 rounding enters the
