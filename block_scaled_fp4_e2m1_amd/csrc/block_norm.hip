@@ -24,7 +24,7 @@
 // Bound by memory: forward 4 H bytes read and 4 H (3 H) written per row, backward
 // 8 H read and 4 H written; the row stays in registers between the reductions.
 // 8192 x 4096: forward 41 us (6.6 TB/s, part of it out of the memory-side cache), backward
-// 96 us (4.2 TB/s): a row's two reductions are waited for with one row ahead in registers.
+// 98 us (4.1 TB/s): a row's two reductions are waited for with one row ahead in registers.
 #include <algorithm>
 
 #include "int8_rows.h"

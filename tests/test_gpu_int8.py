@@ -109,7 +109,9 @@ def test_gemm_largest_sum():
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 4096, 7168), (1, 136, 16), (2, 520, 1040), (3, 512, 8192), (4, 96, 16384),
-                                   (4, 64, 16400), (5, 256, 512), (16, 512, 2048), (40, 264, 7168), (200, 512, 4096)])
+                                   (4, 64, 16400), (5, 256, 512), (16, 512, 2048), (40, 264, 7168), (200, 512, 4096),
+                                   (1, 264, 9472), (1, 520, 9344), (2, 72, 4720), (4, 136, 2320), (4, 40, 2384),
+                                   (3, 8, 48), (4, 7168, 4096)])
 def test_quantize_gemm_is_the_two_calls(M, N, K):
     g = gen(N + K)
     x = rows(g, M, K)
