@@ -395,7 +395,7 @@ bsfp4_status bsfp4_int8_gemm(const int8_t* A, const float* sa, const int8_t* B, 
 }
 
 size_t bsfp4_int8_quantize_gemm_workspace_size(int64_t M, int64_t N, int64_t K) {
-  if (M <= 0 || N <= 0 || K <= 0 || bsfp4::int8_fused_quant_ok(M, K)) return 0;
+  if (M <= 0 || N <= 0 || K <= 0 || bsfp4::int8_fused_quant_ok(M, N, K)) return 0;
   return round256((size_t)M * K) + round256((size_t)M * sizeof(float)) + bsfp4::int8_gemm_workspace(M, N, K);
 }
 
@@ -416,7 +416,7 @@ bsfp4_status bsfp4_int8_quantize_gemm(const uint16_t* x, const int8_t* B, const 
   if (M == 0) return ok();
   if (overlap(D, M * N * 2, x, M * K * 2)) return fail(BSFP4_ERR_INVALID_ARG, "D overlaps x");
   if (bsfp4_status e = check_device()) return e;
-  if (bsfp4::int8_fused_quant_ok(M, K))
+  if (bsfp4::int8_fused_quant_ok(M, N, K))
     return launched(bsfp4::launch_int8_fused_quant_gemm(x, B, sb, bias, D, M, N, K, as_stream(stream)),
                     "bsfp4_int8_quantize_gemm launch");
   int8_t* q = static_cast<int8_t*>(ws);

@@ -14,7 +14,7 @@ size_t int8_gemm_workspace(int64_t M, int64_t N, int64_t K) {
   return tile_workspace(plan_tile(M, N, K, device_cu_count()), M, N);
 }
 
-bool int8_fused_quant_ok(int64_t M, int64_t K) { return rows_quant_ok(M, K); }
+bool int8_fused_quant_ok(int64_t M, int64_t N, int64_t K) { return rows_quant_ok(M, N, K); }
 
 hipError_t launch_int8_fused_quant_gemm(const uint16_t* x, const int8_t* B, const float* sb, const uint16_t* bias,
                                         uint16_t* D, int64_t M, int64_t N, int64_t K, hipStream_t stream) {

@@ -119,8 +119,8 @@ hipError_t launch_int8_quant(const uint16_t* x, int64_t M, int64_t K, int8_t* q,
 
 // 8-bit products (gemm_int8.hip; K % 16 == 0, N % 8 == 0); gated: W [2 I, K].
 size_t int8_gemm_workspace(int64_t M, int64_t N, int64_t K);
-// x quantised inside the product's workgroups (few rows): no intermediate, one launch.
-bool int8_fused_quant_ok(int64_t M, int64_t K);
+// x quantised inside the product's workgroups (few rows, not too many columns): no intermediate, one launch.
+bool int8_fused_quant_ok(int64_t M, int64_t N, int64_t K);
 hipError_t launch_int8_fused_quant_gemm(const uint16_t* x, const int8_t* B, const float* sb, const uint16_t* bias,
                                         uint16_t* D, int64_t M, int64_t N, int64_t K, hipStream_t stream);
 size_t int8_gated_workspace(int64_t M, int64_t I, int64_t K);

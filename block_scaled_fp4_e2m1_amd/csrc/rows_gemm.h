@@ -270,12 +270,18 @@ inline bool rows_ok(int64_t M, int64_t n, int64_t kbytes) {
 }
 
 // 8-bit, the activations x in bf16, up to four rows: where they and their codes (whole
-// 128-byte steps) fit kRowsQuantBytes.  More of them are quantised faster once than by
-// every workgroup: 1 x 4096 x 7168 7.0 us against 9.3 in two launches, 4 x 4096 x 2048 6.0
-// against 6.6; but, read from memory, 2 x 4096 x 7168 9.6 against 9.5 and 4 x 4096 x 7168
-// 12.5 against 9.6.
-inline bool rows_quant_ok(int64_t M, int64_t K) {
-  return M <= 4 && M * ((K + 127) / 128 * 128) + (2 * M * K + 1023) / 1024 * 1024 <= kRowsQuantBytes;
+// 128-byte steps) fit kRowsQuantBytes, K <= 9216 / M.  More of them are quantised faster
+// once than by every workgroup; read from memory, 2 x 4096 x 7168 ran 9.6 us against 9.5
+// and 4 x 4096 x 7168 12.5 against 9.6.  The same holds of many workgroups: each quantises
+// the M K values again, against one launch saved.  Device time, fused against two
+// launches, other weights in turn: 1 x 4096 x 7168 8.0 us against 10.2, 4 x 3584 x 2304
+// 6.0 against 6.2, 2 x 8192 x 1024 5.2 against 6.0, 1 x 131072 x 7168 147 against 153; but
+// 4 x 8192 x 1024 6.5 against 5.9, 4 x 131072 x 1024 69 against 30, 1 x 49152 x 1024 19.0
+// against 17.5.  At either border the two are within 5 %, and the grid stays far below
+// the 2^32 threads of a launch.
+inline bool rows_quant_ok(int64_t M, int64_t N, int64_t K) {
+  return M <= 4 && M * ((K + 127) / 128 * 128) + (2 * M * K + 1023) / 1024 * 1024 <= kRowsQuantBytes &&
+         (M * N <= ((int64_t)1 << 14) || M * M * M * N <= K * K / 128);
 }
 
 inline hipError_t launch_rows_quant(const TileArgs& a, const uint16_t* x, hipStream_t stream) {

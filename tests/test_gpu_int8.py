@@ -164,3 +164,29 @@ def test_empty():
     assert bs.int8_gemm(q, s, W, SW).shape == (0, 32)
     assert bs.int8_quantize_gemm(x, W, SW).shape == (0, 32)
     assert bs.int8_gated_ffn(q, s, W, SW).shape == (0, 16)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 16384, 512), (1, 16392, 512), (4, 4096, 1024), (4, 4104, 1024), (2, 16384, 4096),
+                                   (2, 16392, 4096), (1, 40968, 2048)])
+def test_quantize_gemm_at_the_width_limits(M, N, K):
+    """Both sides of the widths up to which the rows are quantised in the product's workgroups."""
+    g = gen(N + K)
+    x, B, SB = rows(g, M, K), codes(g, N, K), torch.rand(N, generator=g, device=DEV)
+    d = bs.int8_quantize_gemm(x, B, SB)
+    q, s = R.int8_rows(x)
+    ref = R.int8_product(q, s, B, SB)
+    R.check(d, ref, 3.1 * R.F32 * ref.abs(), f"{M}x{N}x{K}")
+    assert torch.equal(d, bs.int8_gemm(*bs.int8_quantize(x), B, SB))
+
+
+def test_quantize_gemm_very_wide():
+    """2^27 columns: 32 threads for each would be more than a launch can hold."""
+    N, K = (1 << 27) + 8, 16
+    g = gen(3)
+    x, B, SB = rows(g, 1, K), codes(g, N, K), torch.rand(N, generator=g, device=DEV)
+    d = bs.int8_quantize_gemm(x, B, SB)
+    c = torch.cat([torch.arange(512, device=DEV), torch.arange(N - 512, N, device=DEV)])
+    q, s = R.int8_rows(x)
+    ref = R.int8_product(q, s, B[c], SB[c])
+    R.check(d[:, c], ref, 3.1 * R.F32 * ref.abs(), "d")
+    assert torch.equal(d, bs.int8_gemm(q, s, B, SB))
