@@ -337,11 +337,12 @@ bsfp4_status check_act(int act) {
   return BSFP4_OK;
 }
 
-// A launch holds fewer than 2^32 threads; the row kernels have at most four times one
-// per eight values, 64 at least.
+// A launch holds fewer than 2^32 threads.  The row kernels of one wave per row launch
+// (rows + 3) / 4 workgroups of 256, the others at most four threads per eight values.
 bsfp4_status check_row_count(int64_t rows, int64_t cols) {
-  if (rows >= (int64_t)1 << 26 || rows * cols >= (int64_t)1 << 33)
-    return fail(BSFP4_ERR_SHAPE, "%lld rows of %lld: need fewer than 2^26 rows and 2^33 values in a call",
+  constexpr int64_t kMostRows = ((int64_t)1 << 26) - 4;
+  if (rows > kMostRows || rows * cols >= (int64_t)1 << 33)
+    return fail(BSFP4_ERR_SHAPE, "%lld rows of %lld: need at most 2^26 - 4 rows and fewer than 2^33 values in a call",
                 (long long)rows, (long long)cols);
   return BSFP4_OK;
 }

@@ -403,7 +403,7 @@ BSFP4_API bsfp4_status nvfp4_moe_grouped_gemm(const uint8_t* Aq, const uint8_t* 
  *   A row of zeros gives s = 0 and q = 0.  A row with an infinity or a NaN
  *   gives s = NaN and q = 0, so every result computed from it is NaN.
  *   x    device bf16 [M, K], M >= 0, K > 0, K % 8 == 0 (the products below
- *        take K % 16 == 0), M < 2^26, M K < 2^33
+ *        take K % 16 == 0), M <= 2^26 - 4, M K < 2^33
  *   q    device int8 [M, K]
  *   s    device float [M]
  *
@@ -500,7 +500,7 @@ BSFP4_API bsfp4_status bsfp4_gated_ffn_backward(const uint16_t* dh, const uint16
  *              overlap them otherwise
  *   z          bf16 [T, H]; or NULL and, instead of it,
  *   q, s       int8 [T, H], float [T]: bsfp4_int8_quantize of z
- *   sizes      T >= 0, H > 0, H % 8 == 0, H <= 16384, T < 2^26, T H < 2^33,
+ *   sizes      T >= 0, H > 0, H % 8 == 0, H <= 16384, T <= 2^26 - 4, T H < 2^33,
  *              groups >= 1, eps > 0
  *
  * bsfp4_block_norm_backward: gradients of the above (z in bf16) from dres_out

@@ -221,3 +221,15 @@ def test_abi_overlapping_outputs(lib):
         for kw in (dict(x=far, residual=FAKE), dict(x=FAKE, residual=far)):
             a = binding.BlockNormArgs(scale=1.0, eps=1e-6, T=4, H=64, groups=1, res_out=res_out, **kw)
             assert lib.bsfp4_block_norm(ctypes.byref(a), None) == INVALID and "overlaps" in err(lib)
+
+
+def test_abi_most_rows(lib):
+    """The row kernels launch 256 threads for every four rows, rounded up: fewer than 2^32 in all."""
+    most = (1 << 26) - 4
+    assert (most + 3) // 4 * 256 < 1 << 32 <= (most + 4) // 4 * 256
+    for rows in (most + 1, most + 3):
+        assert lib.bsfp4_int8_quantize(FAKE, rows, 8, FAKE, FAKE, None) == SHAPE and "rows" in err(lib)
+        a = binding.BlockNormArgs(scale=1.0, eps=1e-6, T=rows, H=8, groups=1, residual=FAKE, w_pre=FAKE, z=FAKE)
+        assert lib.bsfp4_block_norm(ctypes.byref(a), None) == SHAPE and "rows" in err(lib)
+    # `most` itself passes, to be stopped by what is checked after it
+    assert lib.bsfp4_int8_quantize(None, most, 8, FAKE, FAKE, None) == INVALID

@@ -188,3 +188,19 @@ def test_large_norm_batch():
     dx2, dr2, _, _, dg2 = bs.block_norm_backward(residual[rows], x[rows], x[rows], res[rows], gate=gate[g], **kw)
     assert torch.equal(dx[rows], dx2) and torch.equal(dr[rows], dr2)
     assert ((dg[g] - dg2).abs() <= 8 * R.F32 * 3 * dg2.abs().max()).all()
+
+
+def test_most_rows():
+    """As many rows as a launch of the row kernels holds (2^26 - 4), of eight values each."""
+    T, H = (1 << 26) - 4, 8
+    x = big_bf16(T, H, 1.0, 12)
+    w = big_bf16(1, H, 1.0, 13)[0]
+    r = torch.cat([torch.arange(9, device=DEV), torch.arange(T - 9, T, device=DEV)])
+    q, s = bs.int8_quantize(x)
+    wq, ws = R.int8_rows(x[r])
+    assert torch.equal(q[r], wq) and torch.equal(s[r], ws)
+    _, z = bs.block_norm(None, x, w_pre=w)
+    assert torch.equal(z[r], R.norm_steps(None, x[r], None, w, None, 1.0, 1e-6)[1])
+    _, dr, _, dw, _ = bs.block_norm_backward(None, z, None, x, w_pre=w)
+    _, dr2, _, _, _ = bs.block_norm_backward(None, z[r], None, x[r], w_pre=w)
+    assert torch.equal(dr[r], dr2)
