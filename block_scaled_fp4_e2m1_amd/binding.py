@@ -490,7 +490,7 @@ def _run(dev, what, fn, args, size_fn=None, sizes=()):
 
 def int8_quantize(x: torch.Tensor, q: torch.Tensor | None = None, s: torch.Tensor | None = None):
     """bf16 [M, K] -> (8-bit rows int8 [M, K], scales float32 [M]), x ~ q * s per row (token):
-    s = max|x| / 127, q = round-to-even(127 x / max|x|)."""
+    s = max|x| / 127, q = round-to-even(127 x / max|x|).  q and s must not share memory with x."""
     M, K = _matrix(x, _BF16, "x")
     _multiple(K, 8, "K")
     _opt(q, _I8, (M, K), "q")
@@ -514,7 +514,8 @@ def _int8_weight(B, SB, K, name, sname):
 
 
 def int8_gemm(A, SA, B, SB, bias: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
-    """D = bf16((A @ B^T) * SA[:, None] * SB + bias); A int8 [M, K], SA [M], B int8 [N, K], SB [N]."""
+    """D = bf16((A @ B^T) * SA[:, None] * SB + bias); A int8 [M, K], SA [M], B int8 [N, K], SB [N].
+    out must not share memory with an input (here and in the calls below)."""
     M, K = _matrix(A, _I8, "A")
     N = _int8_weight(B, SB, K, "B", "SB")
     _multiple(N, 8, "N")

@@ -14,6 +14,7 @@
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "../../include/bsfp4.h"
@@ -347,10 +348,32 @@ bsfp4_status check_row_count(int64_t rows, int64_t cols) {
   return BSFP4_OK;
 }
 
-// An output that shares memory with an input other workgroups still read.
-bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
-  const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
-  return a != nullptr && b != nullptr && pa < pb + (uintptr_t)nb && pb < pa + (uintptr_t)na;
+struct Span {
+  const void* p;  // null: not given
+  int64_t bytes;
+  const char* name;
+  bool rowwise = false;
+};
+
+bool overlap(const Span& a, const Span& b) {
+  if (a.p == nullptr || b.p == nullptr || a.bytes == 0 || b.bytes == 0) return false;
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+  return pa < pb + (uintptr_t)b.bytes && pb < pa + (uintptr_t)a.bytes;
+}
+
+// No output may share memory with an input that other workgroups still read, nor with
+// another output.  A rowwise output is written by the threads that have read the same
+// place of the rowwise inputs: it may be one of them, but not overlap it otherwise.
+bsfp4_status check_apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (const Span* o = outs.begin(); o != outs.end(); o++) {
+    for (const Span& i : ins)
+      if (overlap(*o, i) && !(o->rowwise && i.rowwise && o->p == i.p))
+        return fail(BSFP4_ERR_INVALID_ARG, "%s overlaps %s%s", o->name, i.name,
+                    o->rowwise && i.rowwise ? " without being it" : "");
+    for (const Span* other = outs.begin(); other != o; other++)
+      if (overlap(*o, *other)) return fail(BSFP4_ERR_INVALID_ARG, "%s overlaps %s", o->name, other->name);
+  }
+  return BSFP4_OK;
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
@@ -367,6 +390,7 @@ bsfp4_status bsfp4_int8_quantize(const uint16_t* x, int64_t M, int64_t K, int8_t
   REQUIRE_PTR(x);
   REQUIRE_PTR(q);
   REQUIRE_SCALAR_PTR(s);
+  if (bsfp4_status e = check_apart({{q, M * K, "q"}, {s, M * 4, "s"}}, {{x, M * K * 2, "x"}})) return e;
   if (bsfp4_status e = check_device()) return e;
   return launched(bsfp4::launch_int8_quant(x, M, K, q, s, as_stream(stream)), "bsfp4_int8_quantize launch");
 }
@@ -390,6 +414,12 @@ bsfp4_status bsfp4_int8_gemm(const int8_t* A, const float* sa, const int8_t* B, 
   if (bias != nullptr && !aligned(bias, 16)) return fail(BSFP4_ERR_ALIGNMENT, "bias is not 16-byte aligned");
   if (bsfp4_status e = check_workspace(ws, ws_bytes, bsfp4_int8_gemm_workspace_size(M, N, K))) return e;
   if (M == 0) return ok();
+  if (bsfp4_status e = check_apart({{D, M * N * 2, "D"}}, {{A, M * K, "A"},
+                                                           {sa, M * 4, "sa"},
+                                                           {B, N * K, "B"},
+                                                           {sb, N * 4, "sb"},
+                                                           {bias, N * 2, "bias"}}))
+    return e;
   if (bsfp4_status e = check_device()) return e;
   return launched(bsfp4::launch_int8_gemm(A, sa, B, sb, bias, D, M, N, K, ws, as_stream(stream)),
                   "bsfp4_int8_gemm launch");
@@ -415,7 +445,9 @@ bsfp4_status bsfp4_int8_quantize_gemm(const uint16_t* x, const int8_t* B, const 
   if (bias != nullptr && !aligned(bias, 16)) return fail(BSFP4_ERR_ALIGNMENT, "bias is not 16-byte aligned");
   if (bsfp4_status e = check_workspace(ws, ws_bytes, bsfp4_int8_quantize_gemm_workspace_size(M, N, K))) return e;
   if (M == 0) return ok();
-  if (overlap(D, M * N * 2, x, M * K * 2)) return fail(BSFP4_ERR_INVALID_ARG, "D overlaps x");
+  if (bsfp4_status e = check_apart({{D, M * N * 2, "D"}},
+                                   {{x, M * K * 2, "x"}, {B, N * K, "B"}, {sb, N * 4, "sb"}, {bias, N * 2, "bias"}}))
+    return e;
   if (bsfp4_status e = check_device()) return e;
   if (bsfp4::int8_fused_quant_ok(M, N, K))
     return launched(bsfp4::launch_int8_fused_quant_gemm(x, B, sb, bias, D, M, N, K, as_stream(stream)),
@@ -448,6 +480,9 @@ bsfp4_status bsfp4_int8_gated_ffn(const int8_t* A, const float* sa, const int8_t
   REQUIRE_PTR(sw);
   if (bsfp4_status e = check_workspace(ws, ws_bytes, bsfp4_int8_gated_ffn_workspace_size(M, I, K))) return e;
   if (M == 0) return ok();
+  if (bsfp4_status e = check_apart({{h, M * I * 2, "h"}},
+                                   {{A, M * K, "A"}, {sa, M * 4, "sa"}, {W, 2 * I * K, "W"}, {sw, I * 8, "sw"}}))
+    return e;
   if (bsfp4_status e = check_device()) return e;
   return launched(bsfp4::launch_int8_gated(A, sa, W, sw, act, h, M, I, K, ws, as_stream(stream)),
                   "bsfp4_int8_gated_ffn launch");
@@ -480,8 +515,9 @@ bsfp4_status bsfp4_gated_ffn(const uint16_t* x, const uint16_t* W, int act, uint
   if (gate_up != nullptr && !aligned(gate_up, 16)) return fail(BSFP4_ERR_ALIGNMENT, "gate_up is not 16-byte aligned");
   if (bsfp4_status e = check_workspace(ws, ws_bytes, bsfp4_gated_ffn_workspace_size(M, I, H))) return e;
   if (M == 0) return ok();
-  if (overlap(h, M * I * 2, x, M * H * 2) || overlap(h, M * I * 2, W, 4 * I * H))
-    return fail(BSFP4_ERR_INVALID_ARG, "h overlaps x or W");
+  if (bsfp4_status e = check_apart({{h, M * I * 2, "h"}, {gate_up, M * I * 8, "gate_up"}},
+                                   {{x, M * H * 2, "x"}, {W, 4 * I * H, "W"}}))
+    return e;
   if (bsfp4_status e = check_device()) return e;
   return launched(bsfp4::launch_gated_ffn(x, W, act, h, gate_up, M, I, H, ws, as_stream(stream)),
                   "bsfp4_gated_ffn launch");
@@ -507,6 +543,11 @@ bsfp4_status bsfp4_gated_ffn_backward(const uint16_t* dh, const uint16_t* x, con
   if (dW != nullptr && !aligned(dW, 16)) return fail(BSFP4_ERR_ALIGNMENT, "dW is not 16-byte aligned");
   if (bsfp4_status e = check_workspace(ws, ws_bytes, bsfp4_gated_ffn_backward_workspace_size(M, I, H))) return e;
   if (M == 0 && dW == nullptr) return ok();
+  // dh and gate_up are read whole before the products write; x is read for dW, W for dx
+  if (bsfp4_status e = check_apart({{dx, M * H * 2, "dx"}, {dW, 4 * I * H, "dW"}},
+                                   {{dW == nullptr ? nullptr : x, M * H * 2, "x"},
+                                    {M == 0 || dx == nullptr ? nullptr : W, 4 * I * H, "W"}}))
+    return e;
   if (bsfp4_status e = check_device()) return e;
   return launched(bsfp4::launch_gated_ffn_bwd(dh, x, W, gate_up, act, M == 0 ? nullptr : dx, dW, M, I, H, ws,
                                               as_stream(stream)),
@@ -581,10 +622,17 @@ bsfp4_status bsfp4_block_norm(const bsfp4_block_norm_args* a, void* stream) {
   if (a->x != nullptr) REQUIRE_FIELD(res_out);
   if (a->w_pre != nullptr && a->z == nullptr && a->q == nullptr)
     return fail(BSFP4_ERR_INVALID_ARG, "w_pre without z or q");
-  const int64_t bytes = 2 * a->T * a->H;
-  for (const uint16_t* in : {a->x, a->residual})
-    if (a->x != nullptr && a->res_out != in && overlap(a->res_out, bytes, in, bytes))
-      return fail(BSFP4_ERR_INVALID_ARG, "res_out overlaps x or residual without being it");
+  const int64_t n = a->T * a->H, vec = 2 * a->H;
+  if (bsfp4_status e = check_apart({{a->x == nullptr ? nullptr : a->res_out, 2 * n, "res_out", true},
+                                    {a->z, 2 * n, "z", true},
+                                    {a->q, n, "q"},
+                                    {a->s, 4 * a->T, "s"}},
+                                   {{a->x, 2 * n, "x", true},
+                                    {a->residual, 2 * n, "residual", true},
+                                    {a->w_post, vec, "w_post"},
+                                    {a->w_pre, vec, "w_pre"},
+                                    {a->gate, vec * a->groups, "gate"}}))
+    return e;
   if (bsfp4_status e = check_device()) return e;
   bsfp4::BlockNormArgs p = norm_args(a);
   p.res_out = a->res_out;
@@ -616,6 +664,21 @@ bsfp4_status bsfp4_block_norm_backward(const bsfp4_block_norm_args* a, void* ws,
   if (a->w_pre != nullptr) REQUIRE_FIELD(dw_pre);
   if (a->gate != nullptr) REQUIRE_FIELD(dgate);
   if (bsfp4_status e = check_workspace(ws, ws_bytes, bsfp4_block_norm_backward_workspace_size(a->T, a->H, a->groups)))
+    return e;
+  const int64_t n = 2 * a->T * a->H, vec = 2 * a->H;
+  const bool pre = a->w_pre != nullptr;
+  if (bsfp4_status e = check_apart({{a->x == nullptr ? nullptr : a->dx, n, "dx", true},
+                                    {a->dres, n, "dres", true},
+                                    {a->w_post == nullptr ? nullptr : a->dw_post, 2 * vec, "dw_post"},
+                                    {pre ? a->dw_pre : nullptr, 2 * vec, "dw_pre"},
+                                    {a->gate == nullptr ? nullptr : a->dgate, 2 * vec * a->groups, "dgate"}},
+                                   {{a->x, n, "x", true},
+                                    {pre ? a->res_out : nullptr, n, "res_out", true},
+                                    {a->dres_out, n, "dres_out", true},
+                                    {a->dz, n, "dz", true},
+                                    {a->w_post, vec, "w_post"},
+                                    {a->w_pre, vec, "w_pre"},
+                                    {a->gate, vec * a->groups, "gate"}}))
     return e;
   if (bsfp4_status e = check_device()) return e;
   bsfp4::BlockNormArgs p = norm_args(a);

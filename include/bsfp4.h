@@ -406,6 +406,9 @@ BSFP4_API bsfp4_status nvfp4_moe_grouped_gemm(const uint8_t* Aq, const uint8_t* 
  *        take K % 16 == 0), M <= 2^26 - 4, M K < 2^33
  *   q    device int8 [M, K]
  *   s    device float [M]
+ * Here and in the calls below an output must not overlap an input or another
+ * output in memory, unless an entry says otherwise: workgroups run in any order.
+ * Such calls are refused with BSFP4_ERR_INVALID_ARG.
  *
  * bsfp4_int8_gemm: D[M,N] = bf16_rne(acc * sa[m] * sb[n] + bias[n]),
  *   acc = sum_k A[m,k] * B[n,k], an exact 32-bit integer; acc -> FP32, the two
@@ -420,7 +423,7 @@ BSFP4_API bsfp4_status nvfp4_moe_grouped_gemm(const uint8_t* Aq, const uint8_t* 
  *            (may be NULL when that is 0); needs no initialisation
  *
  * bsfp4_int8_quantize_gemm: bsfp4_int8_gemm(bsfp4_int8_quantize(x), B) in one
- *   call, bit for bit the output of the two (sizes of both; D must not overlap x).
+ *   call, bit for bit the output of the two (sizes of both).
  *   ws       bsfp4_int8_quantize_gemm_workspace_size(M, N, K) bytes
  *
  * bsfp4_int8_gated_ffn: h[M,I] = bf16_rne(act(G) * U) with [G | U] the scaled
@@ -458,7 +461,7 @@ BSFP4_API bsfp4_status bsfp4_int8_gated_ffn(const int8_t* A, const float* sa, co
  * bsfp4_gated_ffn: [G | U] = x W^T (FP32 sums), h = bf16_rne(act(G) * U).
  *   x        device bf16 [M, H], M >= 0
  *   W        device bf16 [2 I, H]: gate rows, then up rows
- *   h        device bf16 [M, I], not overlapping x or W
+ *   h        device bf16 [M, I]
  *   gate_up  device float [M, 2 I] or NULL: [G | U] for the backward pass
  *   sizes    H > 0, I > 0, multiples of 8, H < 2^22, I < 2^21
  *   ws       bsfp4_gated_ffn_workspace_size(M, I, H) bytes
@@ -468,6 +471,8 @@ BSFP4_API bsfp4_status bsfp4_int8_gated_ffn(const int8_t* A, const float* sa, co
  *     dx = bf16_rne([dG | dU] W),  dW = bf16_rne([dG | dU]^T x)
  *   dx       device bf16 [M, H] or NULL (not computed)
  *   dW       device bf16 [2 I, H] or NULL (not computed); zeros for M == 0
+ *            (both may overlap dh and gate_up, which are read whole first, dx may
+ *            overlap x where dW is not computed, dW W where dx is not)
  *   ws       bsfp4_gated_ffn_backward_workspace_size(M, I, H) bytes
  * Every output is a sum in a fixed order: the same call gives the same bits.
  * ------------------------------------------------------------------------- */
@@ -498,7 +503,8 @@ BSFP4_API bsfp4_status bsfp4_gated_ffn_backward(const uint16_t* dh, const uint16
  *              use gate row g; T % groups == 0
  *   res_out    bf16 [T, H]; may be `residual` or `x` itself, but must not
  *              overlap them otherwise
- *   z          bf16 [T, H]; or NULL and, instead of it,
+ *   z          bf16 [T, H], like res_out possibly `residual` or `x` itself; or
+ *              NULL and, instead of it,
  *   q, s       int8 [T, H], float [T]: bsfp4_int8_quantize of z
  *   sizes      T >= 0, H > 0, H % 8 == 0, H <= 16384, T <= 2^26 - 4, T H < 2^33,
  *              groups >= 1, eps > 0
@@ -511,7 +517,9 @@ BSFP4_API bsfp4_status bsfp4_gated_ffn_backward(const uint16_t* dh, const uint16
  *              residual); required with w_pre
  *   dres_out   bf16 [T, H] or NULL (zeros);  dz  bf16 [T, H], required with
  *              w_pre, else NULL
- *   dx, dres   bf16 [T, H]: gradients of x (required with x) and residual
+ *   dx, dres   bf16 [T, H]: gradients of x (required with x) and residual; each
+ *              may be x, res_out, dres_out or dz itself, but must not overlap them
+ *              otherwise
  *   dw_post, dw_pre  float [H]; dgate  float [groups, H]: required where the
  *              vector is given, NULL elsewhere
  *   ws         bsfp4_block_norm_backward_workspace_size(T, H, groups) bytes

@@ -233,3 +233,106 @@ def test_abi_most_rows(lib):
         assert lib.bsfp4_block_norm(ctypes.byref(a), None) == SHAPE and "rows" in err(lib)
     # `most` itself passes, to be stopped by what is checked after it
     assert lib.bsfp4_int8_quantize(None, most, 8, FAKE, FAKE, None) == INVALID
+
+
+# ---- outputs that share memory with an input or with each other, for every pair of every entry point
+
+M_, N_, K_, T_, H_, G_ = 70, 64, 96, 12, 64, 3
+
+
+def _norm(lib, back):
+    def call(p):
+        a = binding.BlockNormArgs(scale=1.0, eps=1e-6, T=T_, H=H_, groups=G_)
+        for k, v in p.items():
+            setattr(a, k, v)
+        if back:
+            return lib.bsfp4_block_norm_backward(ctypes.byref(a), FAKE, 1 << 30, None)
+        return lib.bsfp4_block_norm(ctypes.byref(a), None)
+    return call
+
+
+#: entry -> (outputs, inputs as name -> bytes, the call, pairs that may be the same memory exactly)
+def overlap_cases(lib):
+    ws = (FAKE, 1 << 30)
+    mk, mn, nk, th, v = M_ * K_, M_ * N_, N_ * K_, 2 * T_ * H_, 2 * H_
+    norm_in = dict(x=th, residual=th, w_post=v, w_pre=v, gate=G_ * v)
+    back_in = dict(x=th, res_out=th, dres_out=th, dz=th, w_post=v, w_pre=v, gate=G_ * v)
+    rows = {(o, i) for o in ("dx", "dres") for i in ("x", "res_out", "dres_out", "dz")}
+    return {
+        "int8_quantize": (dict(q=mk, s=4 * M_), dict(x=2 * mk),
+                          lambda p: lib.bsfp4_int8_quantize(p["x"], M_, K_, p["q"], p["s"], None), set()),
+        "int8_gemm": (dict(D=2 * mn), dict(A=mk, sa=4 * M_, B=nk, sb=4 * N_, bias=2 * N_),
+                      lambda p: lib.bsfp4_int8_gemm(p["A"], p["sa"], p["B"], p["sb"], p["bias"], p["D"], M_, N_, K_, *ws,
+                                                    None), set()),
+        "int8_quantize_gemm": (dict(D=2 * mn), dict(x=2 * mk, B=nk, sb=4 * N_, bias=2 * N_),
+                               lambda p: lib.bsfp4_int8_quantize_gemm(p["x"], p["B"], p["sb"], p["bias"], p["D"], M_, N_,
+                                                                      K_, *ws, None), set()),
+        "int8_gated_ffn": (dict(h=2 * mn), dict(A=mk, sa=4 * M_, W=2 * nk, sw=8 * N_),
+                           lambda p: lib.bsfp4_int8_gated_ffn(p["A"], p["sa"], p["W"], p["sw"], 0, p["h"], M_, N_, K_, *ws,
+                                                              None), set()),
+        "gated_ffn": (dict(h=2 * mn, gate_up=8 * mn), dict(x=2 * mk, W=4 * nk),
+                      lambda p: lib.bsfp4_gated_ffn(p["x"], p["W"], 0, p["h"], p["gate_up"], M_, N_, K_, *ws, None), set()),
+        "gated_ffn_backward": (dict(dx=2 * mk, dW=4 * nk), dict(x=2 * mk, W=4 * nk),
+                               lambda p: lib.bsfp4_gated_ffn_backward(FAKE, p["x"], p["W"], FAKE, 0, p["dx"], p["dW"], M_,
+                                                                      N_, K_, *ws, None), set()),
+        "block_norm": (dict(res_out=th, z=th), norm_in, _norm(lib, False),
+                       {(o, i) for o in ("res_out", "z") for i in ("x", "residual")}),
+        "block_norm int8": (dict(res_out=th, q=th // 2, s=4 * T_), norm_in, _norm(lib, False),
+                            {("res_out", "x"), ("res_out", "residual")}),
+        "block_norm_backward": (dict(dx=th, dres=th, dw_post=2 * v, dw_pre=2 * v, dgate=2 * G_ * v), back_in,
+                                _norm(lib, True), rows),
+    }
+
+
+ENTRIES = ["int8_quantize", "int8_gemm", "int8_quantize_gemm", "int8_gated_ffn", "gated_ffn", "gated_ffn_backward",
+           "block_norm", "block_norm int8", "block_norm_backward"]
+
+
+@pytest.mark.parametrize("entry", ENTRIES)
+def test_abi_every_overlap(lib, entry):
+    outs, ins, call, same = overlap_cases(lib)[entry]
+    every = {**ins, **outs}
+    far = {name: (k + 1) << 36 for k, name in enumerate(every)}
+    for o in outs:
+        for i in every:
+            if i == o:
+                continue
+            # the last 16 bytes, the first, and all of it
+            for at in (far[i] + every[i] // 16 * 16 - 16, far[i] - every[o] // 16 * 16 + 16, far[i]):
+                if at == far[i] and (o, i) in same:
+                    continue
+                assert call({**far, o: at}) == INVALID, (o, i, at - far[i])
+                assert "overlaps" in err(lib) and o in err(lib) and i in err(lib)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are not memory: only where no kernel can be launched")
+@pytest.mark.parametrize("entry", ENTRIES)
+def test_abi_memory_side_by_side(lib, entry):
+    """Neighbours, and outputs that may be an input itself, are not refused: the missing device is what stops them."""
+    outs, ins, call, same = overlap_cases(lib)[entry]
+    every = {**ins, **outs}
+    far = {name: (k + 1) << 36 for k, name in enumerate(every)}
+    after = lambda i: far[i] + (every[i] + 15) // 16 * 16  # noqa: E731
+    none = call(far)
+    assert none not in (OK, INVALID, SHAPE, ALIGN, WORKSPACE)
+    for o in outs:
+        for i in every:
+            if i != o:
+                assert call({**far, o: after(i)}) == none, (o, i)
+                assert call({**far, o: far[i] - (every[o] + 15) // 16 * 16}) == none, (o, i)
+    for o, i in same:
+        assert call({**far, o: far[i]}) == none, (o, i)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are not memory: only where no kernel can be launched")
+def test_abi_backward_over_what_is_not_read(lib):
+    """A gradient may lie over an operand that only the other gradient reads, and over dh and gate_up."""
+    A = [(k + 1) << 36 for k in range(6)]
+
+    def call(dh=A[0], x=A[1], W=A[2], gu=A[3], dx=A[4], dW=A[5]):
+        return lib.bsfp4_gated_ffn_backward(dh, x, W, gu, 0, dx, dW, M_, N_, K_, FAKE, 1 << 30, None)
+
+    none = call()
+    assert none not in (OK, INVALID)
+    assert call(dx=A[1], dW=None) == call(dW=A[2], dx=None) == call(dx=A[0]) == call(dW=A[3]) == none
+    assert call(dx=A[1]) == call(dW=A[2]) == call(dx=A[2], dW=None) == call(dW=A[1], dx=None) == INVALID

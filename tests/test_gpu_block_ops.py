@@ -1,5 +1,7 @@
 """GPU: the block operators as they are used together: a feed-forward block served at 8 bits, one trained in bf16,
 on other streams, and captured into graphs that are replayed with the program's eager work in between."""
+import ctypes
+
 import pytest
 import torch
 
@@ -171,3 +173,78 @@ def test_training_chain_against_differences():
         args = lambda sgn: (r0 + sgn * t * E, w0) if which == 0 else (r0, w0 + sgn * t * E)  # noqa: E731
         diff = (loss(*args(1)) - loss(*args(-1))) / (2 * t)
         assert ((grad * E).sum() - diff).abs() <= 2e-2 * grad.norm()
+
+
+def test_aliased_python_outputs_are_refused():
+    """out= and q= that share memory with an operand other workgroups still read."""
+    K = 128
+    A = torch.randint(-128, 128, (70, K), device=DEV, dtype=torch.int8)
+    W = torch.randint(-128, 128, (128, K), device=DEV, dtype=torch.int8)
+    SA, SW = torch.ones(70, device=DEV), torch.ones(128, device=DEV)
+    x = torch.randn((70, 64), device=DEV).to(torch.bfloat16)
+    before = A.clone(), x.clone()
+    over = A.view(torch.bfloat16)                             # [70, 64] on A's own bytes
+    for call in (lambda: bs.int8_gemm(A, SA, W[:64], SW[:64], out=over), lambda: bs.int8_gated_ffn(A, SA, W, SW, out=over),
+                 lambda: bs.int8_quantize(x, q=x.view(torch.int8).view(-1)[:70 * 64].view(70, 64)),
+                 lambda: bs.int8_quantize(x, s=x.view(-1).view(torch.float32)[:70])):
+        with pytest.raises(bs.Bsfp4Error, match="overlaps"):
+            call()
+    torch.cuda.synchronize()
+    assert torch.equal(A, before[0]) and torch.equal(x, before[1])
+
+
+@pytest.mark.parametrize("T,H", [(300, 512), (700, 4096), (90, 8712)])
+def test_gradients_in_place(T, H):
+    """Row gradients of the norm over their own inputs, and dx of the gated product over an x that is not read."""
+    from block_scaled_fp4_e2m1_amd import binding
+    g = torch.Generator(device=DEV)
+    g.manual_seed(T + H)
+    x, residual, dres, dz = (torch.randn((T, H), generator=g, device=DEV).to(torch.bfloat16) for _ in range(4))
+    wp, wn, gate = (torch.randn(H, generator=g, device=DEV).to(torch.bfloat16) for _ in range(3))
+    kw = dict(w_post=wp, w_pre=wn, gate=gate, scale=0.5)
+    res, z = bs.block_norm(x, residual, **kw)
+    want = bs.block_norm_backward(dres, dz, x, res, **kw)
+    lib = binding.load()
+    n = lib.bsfp4_block_norm_backward_workspace_size(T, H, 1)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    for ox, od in (("x", "res_out"), ("dz", "dres_out"), ("res_out", "x"), ("dres_out", "dz")):
+        t = dict(x=x.clone(), res_out=res.clone(), dres_out=dres.clone(), dz=dz.clone())
+        vecs = [torch.empty(H, device=DEV) for _ in range(3)]
+        a = binding.BlockNormArgs(scale=0.5, eps=1e-6, T=T, H=H, groups=1, w_post=wp.data_ptr(), w_pre=wn.data_ptr(),
+                                  gate=gate.data_ptr(), dx=t[ox].data_ptr(), dres=t[od].data_ptr(),
+                                  **{k: v.data_ptr() for k, v in t.items()},
+                                  **dict(zip(("dw_post", "dw_pre", "dgate"), (v.data_ptr() for v in vecs))))
+        assert lib.bsfp4_block_norm_backward(ctypes.byref(a), ws.data_ptr(), n, torch.cuda.current_stream().cuda_stream) == 0
+        for got, w in zip((t[ox], t[od], *vecs), want):
+            assert torch.equal(got, w)
+    a = binding.BlockNormArgs(scale=0.5, eps=1e-6, T=T, H=H, groups=1, w_pre=wn.data_ptr(), x=x.data_ptr(),
+                              residual=residual.data_ptr())
+    wres, wz = bs.block_norm(x, residual, w_pre=wn, scale=0.5)
+    xi, ri = x.clone(), residual.clone()
+    a.x, a.residual, a.res_out, a.z = xi.data_ptr(), ri.data_ptr(), xi.data_ptr(), ri.data_ptr()
+    assert lib.bsfp4_block_norm(ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(xi, wres) and torch.equal(ri, wz)
+
+
+def test_gated_gradient_over_an_unread_operand():
+    from block_scaled_fp4_e2m1_amd import binding
+    M, H, I = 333, 264, 136
+    g = torch.Generator(device=DEV)
+    g.manual_seed(1)
+    x, dh, W = (torch.randn(s, generator=g, device=DEV).to(torch.bfloat16) for s in ((M, H), (M, I), (2 * I, H)))
+    _, gu = bs.gated_ffn(x, W, save_gate_up=True)
+    dx, dW = bs.gated_ffn_backward(dh, x, W, gu)
+    lib = binding.load()
+    n = lib.bsfp4_gated_ffn_backward_workspace_size(M, I, H)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+
+    def call(dx_at, dW_at, x_at, W_at):
+        st = torch.cuda.current_stream().cuda_stream
+        p = [None if t is None else t.data_ptr() for t in (dh, x_at, W_at, gu)]
+        assert lib.bsfp4_gated_ffn_backward(*p, 0, *(None if t is None else t.data_ptr() for t in (dx_at, dW_at)), M, I, H,
+                                            ws.data_ptr(), n, st) == 0
+
+    xi, Wi = x.clone(), W.clone()
+    call(xi, None, xi, W)
+    call(None, Wi, x, Wi)
+    assert torch.equal(xi, dx) and torch.equal(Wi, dW)
