@@ -9,9 +9,10 @@ def fused(M, N, K):
     return binding.load().bsfp4_int8_quantize_gemm_workspace_size(M, N, K) == 0
 
 
-@pytest.mark.parametrize("M,K", [(1, 9216), (2, 4608), (3, 3072), (4, 2304)])
-def test_fused_quantiser_by_rows(M, K):
+@pytest.mark.parametrize("M", [1, 2, 3, 4])
+def test_fused_quantiser_by_rows(M):
     """Up to where the rows and their codes fit in LDS."""
+    K = 9216 // M
     assert fused(M, 512, K) and not fused(M, 512, K + 16) and not fused(M + 1, 512, K)
 
 

@@ -190,3 +190,54 @@ def test_quantize_gemm_very_wide():
     ref = R.int8_product(q, s, B[c], SB[c])
     R.check(d[:, c], ref, 3.1 * R.F32 * ref.abs(), "d")
     assert torch.equal(d, bs.int8_gemm(q, s, B, SB))
+
+
+def one_call(M, N, K):
+    """Whether int8_quantize_gemm is one launch (no workspace), so that a changed rule cannot empty the tests below."""
+    from block_scaled_fp4_e2m1_amd import binding
+    return binding.load().bsfp4_int8_quantize_gemm_workspace_size(M, N, K) == 0
+
+
+@pytest.mark.parametrize("M,K,one", [(1, 9216, True), (1, 9232, False), (2, 4608, True), (2, 4624, False),
+                                     (3, 3056, True), (3, 3088, False), (4, 2304, True), (4, 2320, False),
+                                     (4, 2032, True), (3, 1008, True), (2, 2320, True), (1, 8208, True), (4, 16, True)])
+@pytest.mark.parametrize("N", [8, 520, 1000])
+def test_quantise_in_the_product(M, K, one, N):
+    """Rows quantised inside the product's workgroups, up to a full LDS area, against 64 bits and the two calls."""
+    assert one_call(M, N, K) == one
+    g = gen(M + N + K)
+    x = rows(g, M, K)
+    B, SB = codes(g, N, K), torch.rand(N, generator=g, device=DEV) + 0.01
+    bias = torch.randn(N, generator=g, device=DEV).to(torch.bfloat16) * 100
+    guard = torch.full((M + 2, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    d = bs.int8_quantize_gemm(x, B, SB, bias=bias, out=guard[1:M + 1])
+    q, s = R.int8_rows(x)
+    ref = R.int8_product(q, s, B, SB)
+    slack = 3 * R.F32 * ref.abs() + R.F32 * (ref.abs() + bias.double().abs())
+    R.check(d, ref + bias.double(), 1.001 * slack, f"{M}x{N}x{K}")
+    assert (guard[0] == 7).all() and (guard[M + 1] == 7).all()
+    assert torch.equal(d, bs.int8_gemm(*bs.int8_quantize(x), B, SB, bias=bias))
+
+
+@pytest.mark.parametrize("M,K", [(1, 9216), (2, 4608), (3, 3056), (4, 2304), (4, 112)])
+@pytest.mark.parametrize("row", [0, -1])
+@pytest.mark.parametrize("value", [0.0, float("inf"), float("-inf"), float("nan")])
+def test_quantise_in_the_product_degenerate_rows(M, K, row, value):
+    """A row of zeros gives zeros (the bias), one infinity or NaN, wherever in the row, a row of NaN; the rows beside
+    it are what they are without it."""
+    N = 136
+    assert one_call(M, N, K)
+    g = gen(M + K)
+    x, B, SB = rows(g, M, K), codes(g, N, K), torch.rand(N, generator=g, device=DEV) + 0.01
+    bias = torch.randn(N, generator=g, device=DEV).to(torch.bfloat16)
+    want = bs.int8_quantize_gemm(x, B, SB, bias=bias)
+    for at in (0, K // 2 + 3, K - 1):
+        y = x.clone()
+        if value == 0.0:
+            y[row] = 0.0
+        else:
+            y[row, at] = value
+        d = bs.int8_quantize_gemm(y, B, SB, bias=bias)
+        others = [m for m in range(M) if m != row % M]
+        assert torch.equal(d[others], want[others])
+        assert torch.equal(d[row], bias) if value == 0.0 else d[row].isnan().all()
