@@ -211,3 +211,54 @@ def test_empty():
     assert res.shape == z.shape == (0, 64)
     dx, dr, dwp, dwn, dg = bs.block_norm_backward(dres[:0], dz[:0], p["x"][:0], res, **kw)
     assert dx.shape == dr.shape == (0, 64) and (dwp == 0).all() and (dwn == 0).all() and (dg == 0).all()
+
+
+def additions(T, H, groups):
+    """The longest chain of additions behind a vector gradient: the rows of a strip one by one, then the strips'
+    partials (every 64th in one thread, the 64 threads' in two steps and fifteen more additions)."""
+    chunks, nt = H // 8, 64
+    while nt < min(1024, chunks):
+        nt *= 2
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    want = min(min(1024, cus * (1024 // nt)), max(min(T, cus), T // 4))
+    if groups >= want:
+        per = -(-groups // want)
+        strips, rows = -(-groups // per), per * (T // groups)
+    else:
+        parts = min(T // groups, -(-want // groups))
+        strips, rows = groups * parts, -(-(T // groups) // parts)
+    return rows + -(-strips // 64) + 17
+
+
+@pytest.mark.parametrize("T,H,groups", [(8192, 4096, 1), (1500, 8192, 1), (1100, 16384, 2), (2050, 8200, 1), (6000, 7168, 3),
+                                        (9000, 2048, -1), (9000, 264, 3000), (20000, 512, 5)])
+@pytest.mark.parametrize("parts", ["all", "no_post", "no_pre", "pre_only", "no_dres", "no_gate"])
+def test_backward_many_rows_per_strip(T, H, groups, parts):
+    """Every output against 64 bits where a workgroup walks several rows, at every width of the kernels.  A vector's
+    gradient: its terms' 64 roundings, and one for every addition that a term passes through."""
+    p, dres, dz = problem(T, H, groups, seed=13)
+    if parts == "no_post":
+        p["w_post"] = None
+    if parts == "no_pre":
+        p["w_pre"], dz = None, None
+    if parts == "pre_only":
+        p["x"] = p["w_post"] = p["gate"] = None
+    if parts == "no_dres":
+        dres = None
+    if parts == "no_gate":
+        p["gate"] = None
+    kw = dict(w_post=p["w_post"], w_pre=p["w_pre"], gate=p["gate"], scale=0.3, eps=EPS)
+    fwd = bs.block_norm(p["x"], p["residual"], **kw)
+    res = fwd[0] if p["w_pre"] is not None else fwd
+    names = ("dx", "dres", "dw_post", "dw_pre", "dgate")
+    got = dict(zip(names, bs.block_norm_backward(dres, dz, p["x"], res if dz is not None else None, **kw)))
+    want = reference_backward(dres, dz, p, res, 0.3)
+    assert {n for n in names if got[n] is not None} == set(want)
+    n_add = additions(T, H, 1 if p["gate"] is None else p["gate"].reshape(-1, H).shape[0])
+    assert T <= 1024 or n_add < T // 2  # a bound far below one by the number of rows
+    for n, (ref, mag) in want.items():
+        if n in ("dx", "dres"):
+            R.check(got[n], ref, 64 * R.F32 * mag, f"{n} {parts}")
+        else:
+            err, bound = (got[n].double() - ref).abs(), (64 + n_add) * R.F32 * mag + 1e-40
+            assert (err <= bound).all(), (n, (err / bound).max().item())
