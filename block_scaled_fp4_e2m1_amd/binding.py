@@ -582,7 +582,8 @@ def _gated_args(x, W13):
 
 def gated_ffn(x, W13, act="silu", save_gate_up: bool = False, out: torch.Tensor | None = None):
     """h = bf16(act(G) * U), [G | U] = x @ W13^T; x bf16 [M, H], W13 bf16 [2 I, H] (gate rows, then up rows).
-    With save_gate_up returns (h, float32 [G | U]) for gated_ffn_backward."""
+    With save_gate_up returns (h, float32 [G | U]) for gated_ffn_backward.  Outputs carry no autograd history,
+    whatever the inputs do: gradients come from gated_ffn_backward only."""
     a = _act(act)
     M, H, I = _gated_args(x, W13)
     _opt(out, _BF16, (M, I), "out")
@@ -654,7 +655,8 @@ def block_norm(x, residual, w_post=None, w_pre=None, gate=None, scale: float = 1
     x, residual bf16 [T, H]; w_post, w_pre bf16 [H]; gate bf16 [H] or [groups, H] (T / groups consecutive
     rows each).  Without w_post x is added as it is; without x only z = rms_norm(residual, w_pre) is computed
     and res is residual itself.  Returns (res, z), (res, q, s) for fmt="int8" (z quantised per token as by
-    int8_quantize) or res alone without w_pre.  res_out may be residual (in place)."""
+    int8_quantize) or res alone without w_pre.  res_out may be residual or x (in place), but not overlap an input
+    otherwise.  Outputs carry no autograd history: gradients come from block_norm_backward only."""
     if fmt not in ("bf16", "int8"):
         raise ValueError(f"unknown output format {fmt!r} (bf16 or int8)")
     T, H, groups = _norm_args(x, residual, "residual", w_post, w_pre, gate, eps)

@@ -114,7 +114,7 @@ hipError_t launch_nvfp4_grouped(const uint8_t* Aq, const uint8_t* Asf, const int
                                 int64_t N, int64_t K, int epilogue, uint16_t* out, uint8_t* out_q, uint8_t* out_sf,
                                 const float* out_gs, const int32_t* sorted_ids, float* y, hipStream_t stream);
 
-// Per-token 8-bit rows of a bf16 matrix (K % 16 == 0).
+// Per-token 8-bit rows of a bf16 matrix (K % 8 == 0).
 hipError_t launch_int8_quant(const uint16_t* x, int64_t M, int64_t K, int8_t* q, float* s, hipStream_t stream);
 
 // 8-bit products (gemm_int8.hip; K % 16 == 0, N % 8 == 0); gated: W [2 I, K].

@@ -15,9 +15,9 @@
 // and chunks past K are zeros through the buffers' range check.  The waves' sums are
 // added in wave order by one wave, which finishes the outputs.
 //
-// Bound by the weight's bytes from some 20 MB on: bf16 gated 1 x 14336 x 4096 (117 MB)
-// 20.7 us, 5.7 TB/s out of the memory-side cache, 41 us from HBM behind dirty lines; int8
-// 8 x 65536 x 4096 (268 MB) 48 us, 5.6 TB/s.  Smaller ones are a launch and two memory
+// Bound by the weight's bytes from some 20 MB on: bf16 gated 1 x 14336 x 4096 (117 MB) 21
+// us, 5.6 TB/s, behind other data (42 where that was written just before: its lines go back
+// to memory meanwhile); int8 8 x 65536 x 4096 (268 MB) 48 us, 5.6 TB/s.  Smaller ones are a launch and two memory
 // latencies (int8 16 x 1024 x 4096 3.5 us).
 //
 // kQuant (8-bit): the activations come in bf16 and every workgroup quantises all of

@@ -35,9 +35,10 @@
 // chunks run through the same loop.
 //
 // Measured at 4096 x 4096 x 7168 (256 x 256 tiles): bf16 158 us, 1.52 PFLOP/s; int8
-// 85.7 us, 2.81 POP/s.  The matrix cores are busy three quarters of the time and the clock
-// drops under them; the rest is the wait at each stage's barrier, which two slots
-// of 64 KB do not cover.
+// 85.7 us, 2.81 POP/s (98, 2.45, on the slowest card seen).  The matrix cores are busy 62
+// to 75 % of the time (counters: gated forward 62, int8 71, the gradients 73 and 75) at
+// 1.7 to 1.9 GHz; the rest is the wait at each stage's barrier, which two slots of 64 KB
+// do not cover, and the epilogue.
 #pragma once
 
 #include <algorithm>
@@ -113,7 +114,8 @@ __device__ __forceinline__ void act_value_grad(int act, float g, float& a, float
 // Position of 16-byte chunk c of row r inside its 128 bytes is c ^ tile_swz(r).  A
 // fragment's read (row lane % 16, chunk lane / 16) is served 16 lanes at a time,
 // lanes 0-3, 12-15 and 20-27 first, 4-11, 16-19 and 28-31 next: with r % 8 each of these
-// sixteen meets other banks (no conflicts counted; r ^ r / 8 % 2 doubled every read).
+// sixteen meets other banks (r ^ r / 8 % 2 doubled every read; of a kernel's LDS cycles 1
+// to 5 % are counted as conflicts, half were so).
 __device__ __forceinline__ constexpr int tile_swz(int r) { return r & 7; }
 
 // Transposed: 32-byte unit u (16 values) of k row k is kept at u ^ tile_tswz(k).  A
@@ -658,7 +660,7 @@ struct TilePlan {
 // estimated time.  A stage takes a workgroup us[c - 1] microseconds when c share a
 // compute unit, its start and end round_us; a split's second kernel costs kSplitUs
 // and its partials their bytes.  The figures are a least-squares fit to 2034 timed
-// (shape, kernel, split) combinations, M 48 .. 4096, weights of 1536 x 2048 .. 14336 x
+// (shape, kernel, split) combinations (profiles/tile_plan_timings.csv), M 48 .. 4096, weights of 1536 x 2048 .. 14336 x
 // 4096, bf16 and int8 (9 % rms); the plan's choice is 0.4 % slower than the best of
 // each shape on average, 8 % at worst.  N counts weight rows (gated: both halves).
 struct TileCost {
