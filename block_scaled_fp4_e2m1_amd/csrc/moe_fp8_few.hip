@@ -327,9 +327,11 @@ __global__ void __launch_bounds__(512, 2)
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     if (i + RING < mine) issue(item_of(i + RING), slot);
     const v4f part = mfma_fp8(fp8_frag(w[0], w[1]), fp8_frag(x[0], x[1]));
-    const float f = r >= 0 ? sx * sw * wt : 0.0f;  // a token that does not go there: its row is another's, finite or not
+    // a token that does not go there keeps its sum: its row is another's, and a NaN among the weight's codes or scales would
+    // outlast a factor of zero
+    const float f = sx * sw * wt;
 #pragma unroll
-    for (int k = 0; k < 4; k++) acc[k] = __builtin_fmaf(part[k], f, acc[k]);
+    for (int k = 0; k < 4; k++) acc[k] = r >= 0 ? __builtin_fmaf(part[k], f, acc[k]) : acc[k];
   };
   int i = 0, slot = 0;
   for (; i < mine; i++) {
