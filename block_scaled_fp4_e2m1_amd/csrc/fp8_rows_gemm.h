@@ -200,18 +200,6 @@ inline hipError_t launch_fp8_rows(const Fp8Args& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Whether M rows run on fp8_rows: 64 steps a wave at most, and few enough columns that its workgroups, which read all
-// activations each, beat tiles.  us against tiles, other weights in turn: 1 x 4096 x 7168 7.3, 11.1; 16 x 512 x 512 2.6,
-// 4.0; 32 x 4096 x 7168 9.3, 12.4; 16 x 131072 x 4096 106, 116; but 32 x 14336 x 4096 16.7, 15.1; 24 x 16384 x 7168 29,
-// 25.5.  Short K leaves its workgroups little beside their start: 1 x 65536 x 1024 19.2, 16; 8 x 32768 x 1024 10.4, 8.9;
-// 8 x 16384 x 2048 8.4, 8.8; 16 x 8192 x 512 3.4, 4.4.
-inline bool fp8_rows_ok(int64_t M, int64_t N, int64_t K) {
-  const int64_t waves = M <= 16 ? 8 : 4;
-  if (M > kFp8RowsMaxM || fp8_blocks(K) > 64 * waves) return false;
-  if (M <= 16 && K >= 4096) return M * N <= (int64_t)1 << 21;
-  return M * N <= (int64_t)1 << 18 && N <= std::max<int64_t>(8192, 8 * K);
-}
-
 // Up to four rows in bf16, quantised inside: what fits in LDS, and where it is cheaper than a launch of its own.  us,
 // inside against two launches: 1 x 4096 x 7168 7.8, 10.1; 4 x 512 x 512 4.0, 4.9; 2 x 14336 x 4096 13.4, 15.2; but 3 x
 // 65536 x 1024 26.6, 21.8.
@@ -219,6 +207,23 @@ inline bool fp8_rows_quant_ok(int64_t M, int64_t N, int64_t K) {
   const int64_t lds = (M * fp8_blocks(K) * (kFp8Block + 4) + 15) / 16 * 16 + (2 * M * K + 1023) / 1024 * 1024;
   return M <= 4 && fp8_blocks(K) <= 512 && lds <= kFp8RowsQuantBytes &&
          (M * N <= ((int64_t)1 << 14) || M * M * M * N <= K * K / 128);
+}
+
+// Whether M rows run on fp8_rows: 64 steps a wave at most, and few enough columns that its workgroups, which read all
+// activations each, beat tiles.  us against tiles, other weights in turn: 1 x 4096 x 7168 7.3, 11.1; 16 x 512 x 512 2.6,
+// 4.0; 32 x 4096 x 7168 9.3, 12.4; 16 x 131072 x 4096 106, 116; but 32 x 14336 x 4096 16.7, 15.1; 24 x 16384 x 7168 29,
+// 25.5.  Short K leaves its workgroups little beside their start: 1 x 65536 x 1024 19.2, 16; 8 x 32768 x 1024 10.4, 8.9;
+// 8 x 16384 x 2048 8.4, 8.8; 16 x 8192 x 512 3.4, 4.4.
+//
+// What may be quantised inside always runs here, so that the product alone sums in the same order and gives the same bits.
+// Beyond the other bounds that is one row of more columns (10000 x 512 4.2, 4.4; 16384 x 512 4.8, 4.6; 16384 x 1024 6.5, 6.3;
+// 32768 x 2048 15.2, 15.5; 49152 x 2560 24.9, 30.6; quantised inside 5.1, 5.8, 7.4, 15.4, 25.1, on tiles behind the quantiser
+// 6.7, 7.0, 9.0, 17.1, 30.5).
+inline bool fp8_rows_ok(int64_t M, int64_t N, int64_t K) {
+  const int64_t waves = M <= 16 ? 8 : 4;
+  if (M > kFp8RowsMaxM || fp8_blocks(K) > 64 * waves) return false;
+  if (M <= 16 && K >= 4096) return M * N <= (int64_t)1 << 21;
+  return (M * N <= (int64_t)1 << 18 && N <= std::max<int64_t>(8192, 8 * K)) || fp8_rows_quant_ok(M, N, K);
 }
 
 inline hipError_t launch_fp8_rows_quant(const Fp8Args& a, const uint16_t* x, hipStream_t stream) {
