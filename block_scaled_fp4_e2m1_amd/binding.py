@@ -1013,7 +1013,7 @@ def fp8_moe_grouped_gemm(Aq, As, expert_offsets, W, Ws, epilogue=MOE_STORE_BF16,
     a_row_index int32 [rows] row m reads row a_row_index[m] of Aq; otherwise rows = A.  Rows past the last expert's give zeros.
     MOE_STORE_BF16: bf16 [rows, N].  MOE_SILU_MUL_QUANT: silu(gate) * up of the gate and up halves of N, quantised:
     (out_q [rows, N / 2], out_s [N / 256, rows]).  MOE_WEIGHTED_COMBINE: bf16 [T, N], each token's rows row_of [T, topk] times
-    topk_weights, summed."""
+    topk_weights, summed.  An output that the epilogue does not write is refused."""
     A, K = _matrix(Aq, _F8, "Aq")
     E, N, KW = _cube(W, _F8, "W")
     if KW != K:
@@ -1039,6 +1039,9 @@ def fp8_moe_grouped_gemm(Aq, As, expert_offsets, W, Ws, epilogue=MOE_STORE_BF16,
     elif epilogue not in (MOE_STORE_BF16, MOE_SILU_MUL_QUANT):
         raise ValueError(f"unknown epilogue {epilogue!r}")
     quant = epilogue == MOE_SILU_MUL_QUANT
+    for t, name, written in ((out, "out", not quant), (out_q, "out_q", quant), (out_s, "out_s", quant)):
+        if t is not None and not written:
+            raise ValueError(f"{name} is not written by this epilogue")
     if quant:
         _opt(out_q, _F8, (rows, N // 2), "out_q")
         _opt(out_s, _F32, (N // 256, rows), "out_s")
@@ -1047,13 +1050,12 @@ def fp8_moe_grouped_gemm(Aq, As, expert_offsets, W, Ws, epilogue=MOE_STORE_BF16,
     dev = _gpu("Aq As expert_offsets W Ws a_row_index out out_q out_s row_of topk_weights", Aq, As, expert_offsets, W, Ws,
                a_row_index, out, out_q, out_s, row_of, topk_weights)
     if quant:
-        out = None
         out_q = Aq.new_empty((rows, N // 2)) if out_q is None else out_q
         out_s = As.new_empty((N // 256, rows)) if out_s is None else out_s
     elif out is None:
         out = Aq.new_empty((T if epilogue == MOE_WEIGHTED_COMBINE else rows, N), dtype=_BF16)
-    ep = Fp8MoeEpilogueArgs(out=_a(out), out_q=_a(out_q) if quant else None, out_s=_a(out_s) if quant else None,
-                            row_of=_a(row_of), topk_weights=_a(topk_weights), num_tokens=T, topk=topk)
+    ep = Fp8MoeEpilogueArgs(out=_a(out), out_q=_a(out_q), out_s=_a(out_s), row_of=_a(row_of),
+                            topk_weights=_a(topk_weights), num_tokens=T, topk=topk)
     lib = load()
     _run(dev, "bsfp4_fp8_moe_grouped_gemm", lib.bsfp4_fp8_moe_grouped_gemm,
          (Aq.data_ptr(), As.data_ptr(), A, _a(a_row_index), expert_offsets.data_ptr(), E, rows, W.data_ptr(),
