@@ -863,24 +863,34 @@ def fp8_linear_backward(dy, x, WT, SWT, need_dx: bool = True, need_dW: bool = Tr
     one that is not needed.
 
     dy bf16 [M, N], x bf16 [M, K]; WT [K, N] and SWT [ceil(K / 128), ceil(N / 128)] the transposed weight of
-    fp8_quantize_weight.  dy is quantised along N for dx; dy and x along M for dW."""
+    fp8_quantize_weight.  dy is quantised along N for dx; dy and x along M for dW.  x may be None without need_dW, WT and SWT
+    without need_dx."""
     M, N = _matrix(dy, _BF16, "dy")
-    MX, K = _matrix(x, _BF16, "x")
-    if MX != M:
-        raise ValueError(f"dy has {M} rows but x has {MX}")
-    _multiple(N, 16, "N")
-    _multiple(K, 16, "K")
-    _as(WT, _F8, (K, N), "WT")
-    _as(SWT, _F32, (_blocks(K), _blocks(N)), "SWT")
-    dev = _gpu("dy x WT SWT", dy, x, WT, SWT)
-    dx = torch.empty_like(x) if need_dx else None
     f32 = _float_or_bf16(dW_dtype, "dW_dtype")
-    dW = x.new_empty((N, K), dtype=dW_dtype) if need_dW else None
+    if need_dW and x is None:
+        raise ValueError("dW needs x")
+    if need_dx and (WT is None or SWT is None):
+        raise ValueError("dx needs WT and SWT")
+    _multiple(N, 16, "N")
+    K = None
+    if x is not None:
+        MX, K = _matrix(x, _BF16, "x")
+        if MX != M:
+            raise ValueError(f"dy has {M} rows but x has {MX}")
+    elif WT is not None:
+        K = _matrix(WT, _F8, "WT")[0]
+    if K is not None:
+        _multiple(K, 16, "K")
+        _opt(WT, _F8, (K, N), "WT")
+        _opt(SWT, _F32, (_blocks(K), _blocks(N)), "SWT")
+    dev = _gpu("dy x WT SWT", dy, x, WT, SWT)
+    dx = dy.new_empty((M, K)) if need_dx else None
+    dW = dy.new_empty((N, K), dtype=dW_dtype) if need_dW else None
     if dx is None and dW is None:
         return None, None
     lib = load()
     _run(dev, "bsfp4_fp8_linear_backward", lib.bsfp4_fp8_linear_backward,
-         (dy.data_ptr(), x.data_ptr(), WT.data_ptr(), SWT.data_ptr(), _a(dx), _a(dW), f32, M, N, K),
+         (dy.data_ptr(), _a(x), _a(WT), _a(SWT), _a(dx), _a(dW), f32, M, N, K),
          lib.bsfp4_fp8_linear_backward_workspace_size, (M, N, K, need_dx, need_dW))
     return dx, dW
 

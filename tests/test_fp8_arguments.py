@@ -1,5 +1,6 @@
 """CPU: arguments of the E4M3 operators that a call does not need (meta tensors, nothing reaches the library)."""
 import pytest
+import torch
 
 import block_scaled_fp4_e2m1_amd as bs
 from test_block_ops_refusals import reaches_device_check, refused
@@ -17,3 +18,20 @@ def test_grouped_outputs_that_are_not_written(epilogue, more, good, bad):
     for name, t in bad.items():
         refused(f"{name} is not written", bs.fp8_moe_grouped_gemm, *args, **more, **{name: t})
         refused(f"{name} is not written", bs.fp8_moe_grouped_gemm, *args, **more, **good, **{name: t})
+
+
+def test_linear_backward_without_what_it_does_not_read():
+    dy, x, WT, SWT = m(5, 144), m(5, 272), q(272, 144), f(3, 2)
+    b = bs.fp8_linear_backward
+    reaches_device_check(b, dy, None, WT, SWT, need_dW=False)
+    reaches_device_check(b, dy, x, None, None, need_dx=False)
+    reaches_device_check(b, dy, None, None, None, need_dx=False, need_dW=False)
+    refused("dW needs x", b, dy, None, WT, SWT)
+    refused("dx needs WT and SWT", b, dy, x, None, SWT)
+    refused("dx needs WT and SWT", b, dy, x, WT, None)
+    # what is given all the same is held to its shape
+    refused("dy has 5 rows but x has 6", b, dy, m(6, 272), WT, SWT, need_dW=False)
+    refused("WT must have", b, dy, x, q(144, 272), SWT, need_dx=False)
+    refused("SWT must have", b, dy, None, WT, f(2, 3), need_dW=False)
+    refused("multiple of 16", b, dy, None, q(264, 144), f(3, 2), need_dW=False)
+    refused("dW_dtype", b, dy, x, WT, SWT, dW_dtype=torch.float16)
