@@ -1,4 +1,4 @@
-// Which kernel an E4M3 product runs on.
+// Which kernel an E4M3 product runs on, dense or grouped by expert.
 #pragma once
 
 #include "fp8_rows_gemm.h"
@@ -67,6 +67,21 @@ inline TileKind plan_fp8_gradients(int64_t M, int64_t N, int64_t K, int cus) {
     if (t < best) best = t, kind = k;
   }
   return kind;
+}
+
+// Grouped by expert, N columns of results: whether a tile has up to 256 rows, or 64.
+//
+// Tiles of 64 rows while each expert has few, and while they all run at once (rows / 64 and half a tile an expert;
+// one workgroup a CU of the gated kernel, two of the other): a taller tile only leaves CUs idle then.  Beyond, a
+// taller tile reads the weight less often.  us, tiles of 64 against up to 256 rows (H, I, experts x rows each):
+//   up    1024, 512, 16 x 192: 12 against 23; 4096, 2048, 8 x 96: 34, 41; 7168, 2048, 16 x 64: 127, 94;
+//         4096, 1024, 32 x 32: 88, 66 (an expert with more than 64); 4096, 2048, 128 x 16: the same
+//   down  2048, 2048, 16 x 96: 19 against 26; 3584, 1024, 60 x 16: 52, 57; 4096, 512, 128 x 128: 157, 122
+inline bool fp8_tall_tiles(bool gated, int64_t rows, int64_t N, int64_t E, int cus) {
+  const int64_t slots = gated ? cus : 2 * cus;
+  const int64_t mean = rows / std::min<int64_t>(E, std::max<int64_t>(rows, 1));
+  const int64_t tiles = (rows + 32 * E) / 64 * ((N + 127) / 128);
+  return mean > 24 && tiles > slots;
 }
 
 // Few rows: a scale per block of B, a bf16 result.

@@ -1,6 +1,6 @@
 // E4M3 products over rows sorted by expert, each expert with its own weight: gate and up with silu(gate) * up quantised
 // again in the epilogue, and down.
-#include "fp8_tile.h"
+#include "fp8_plan.h"
 
 namespace bsfp4 {
 namespace {
@@ -13,16 +13,7 @@ hipError_t launch_by_rows(Fp8Args a, hipStream_t stream) {
     a.tiles_n = (a.N + cols - 1) / cols;
     return (unsigned)((int64_t)a.tiles_m * a.tiles_n);
   };
-  // Tiles of 64 rows while each expert has few, and while they all run at once (rows / 64 and half a tile an expert;
-  // one workgroup a CU of the gated kernel, two of the other): a taller tile only leaves CUs idle then.  Beyond, a
-  // taller tile reads the weight less often.  us, tiles of 64 against up to 256 rows (H, I, experts x rows each):
-  //   up    1024, 512, 16 x 192: 12 against 23; 4096, 2048, 8 x 96: 34, 41; 7168, 2048, 16 x 64: 127, 94;
-  //         4096, 1024, 32 x 32: 88, 66 (an expert with more than 64); 4096, 2048, 128 x 16: the same
-  //   down  2048, 2048, 16 x 96: 19 against 26; 3584, 1024, 60 x 16: 52, 57; 4096, 512, 128 x 128: 157, 122
-  constexpr int kSlots = EPI == kFp8Gated ? 256 : 512;
-  const int64_t mean = (int64_t)a.M / std::min<int64_t>(a.E, std::max(a.M, 1));
-  const int64_t tiles = ((int64_t)a.M + 32 * a.E) / 64 * ((a.N + 127) / 128);
-  if (mean > 24 && tiles > kSlots) {
+  if (fp8_tall_tiles(EPI == kFp8Gated, a.M, a.N, a.E, device_cu_count())) {
     const unsigned n = grid(256, EPI == kFp8Gated ? 128 : 256);
     fp8_grouped_many<EPI><<<n, 512, 0, stream>>>(a);
   } else if constexpr (EPI == kFp8Gated) {

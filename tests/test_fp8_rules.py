@@ -2,6 +2,8 @@
 import subprocess
 
 from block_scaled_fp4_e2m1_amd import build
+from test_gpu_fp8_moe import GROUPS
+from test_gpu_fp8_plans import HEIGHTS
 
 FEW_ROWS = r"""
 #include <cstdio>
@@ -33,3 +35,31 @@ def test_rows_quantised_inside_are_rows(tmp_path):
     lines = run(tmp_path, FEW_ROWS)
     inside, apart = map(int, lines[-1].split())
     assert inside > 100000 and apart == 0, lines
+
+
+HEIGHT = r"""
+#include <cstdio>
+#include "fp8_plan.h"
+int main() {
+  long long gated, rows, n, e, cus;
+  while (std::scanf("%lld %lld %lld %lld %lld", &gated, &rows, &n, &e, &cus) == 5)
+    std::printf("%d\n", (int)bsfp4::fp8_tall_tiles(gated, rows, n, e, (int)cus));
+}
+"""
+
+
+def test_grouped_heights(tmp_path):
+    """The shapes that are to run on tall tiles and on tiles of 64 rows do, with either epilogue; the border moves with the chip."""
+    shapes, want = [], []
+    for tall, groups in ((True, HEIGHTS), (False, GROUPS)):
+        for counts, behind, N, _ in groups:
+            rows = sum(counts) + behind
+            shapes += [(0, rows, N, len(counts), 256), (1, rows, N // 2, len(counts), 256)]
+            want += [tall] * 2
+    for gated in (0, 1):
+        # 48 experts of 60 rows: (2880 + 1536) / 64 = 69 row tiles of 8 columns' blocks, 552 in all
+        for cus in (32, 256, 304):
+            shapes.append((gated, 2880, 1024, 48, cus))
+            want.append(552 > (cus if gated else 2 * cus))
+    text = "\n".join(" ".join(map(str, s)) for s in shapes)
+    assert [int(v) for v in run(tmp_path, HEIGHT, text)] == want
