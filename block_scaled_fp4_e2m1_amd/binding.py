@@ -816,7 +816,9 @@ def _float_or_bf16(dtype, name):
 
 def fp8_gemm(A, SA, B, SB, bias: torch.Tensor | None = None, out_dtype=torch.bfloat16,
              out: torch.Tensor | None = None) -> torch.Tensor:
-    """D = dequant(A) @ dequant(B)^T + bias in FP32 sums, rounded to out_dtype (bfloat16 or float32) once.
+    """D = dequant(A) @ dequant(B)^T + bias, rounded to out_dtype (bfloat16 or float32) once.  FP32 sums of the matrix cores'
+    sums of eight products, which leave out what is below 2^-13 of the largest one's binade: some 1.5e-5 of a result on random
+    values, in a float32 result as well.
 
     A [M, K], B [N, K] E4M3 codes; SA [ceil(K / 128), M]; SB [ceil(N / 128), ceil(K / 128)] (fp8_quantize_weight) or
     [ceil(K / 128), N] (fp8_quantize).  A float32 result takes no bias.  out must not share memory with an input."""
@@ -863,8 +865,8 @@ def fp8_linear_backward(dy, x, WT, SWT, need_dx: bool = True, need_dW: bool = Tr
     one that is not needed.
 
     dy bf16 [M, N], x bf16 [M, K]; WT [K, N] and SWT [ceil(K / 128), ceil(N / 128)] the transposed weight of
-    fp8_quantize_weight.  dy is quantised along N for dx; dy and x along M for dW.  x may be None without need_dW, WT and SWT
-    without need_dx."""
+    fp8_quantize_weight.  dy is quantised along N for dx; dy and x along M for dW; sums as fp8_gemm's.  x may be None without
+    need_dW, WT and SWT without need_dx."""
     M, N = _matrix(dy, _BF16, "dy")
     f32 = _float_or_bf16(dW_dtype, "dW_dtype")
     if need_dW and x is None:
@@ -1017,7 +1019,8 @@ def _cube(t, dtype, name):
 
 def fp8_moe_grouped_gemm(Aq, As, expert_offsets, W, Ws, epilogue=MOE_STORE_BF16, *, a_row_index=None, out=None, out_q=None,
                          out_s=None, row_of=None, topk_weights=None):
-    """Grouped E4M3 product over rows sorted by expert: rows [expert_offsets[e], expert_offsets[e + 1]) times W[e].
+    """Grouped E4M3 product over rows sorted by expert: rows [expert_offsets[e], expert_offsets[e + 1]) times W[e], sums as
+    fp8_gemm's.
 
     Aq [A, K] codes, As [ceil(K / 128), A]; W [E, N, K], Ws [E, ceil(N / 128), ceil(K / 128)] (fp8_quantize_weight).  With
     a_row_index int32 [rows] row m reads row a_row_index[m] of Aq; otherwise rows = A.  Rows past the last expert's give zeros.

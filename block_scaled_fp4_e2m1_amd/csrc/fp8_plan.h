@@ -6,7 +6,8 @@
 namespace bsfp4 {
 namespace {
 
-// Costs as in kTileCosts, fitted to 5795 timed (shape, kernel, split) combinations (profiles/fp8_tile_plan_timings.csv):
+// Costs as in kTileCosts, fitted to 5795 timed (shape, kernel, split) combinations (profiles/fp8_tile_plan_timings.csv) by
+// least squares of log(tile_time and the split's cost / time), residuals past 0.1 weighted down:
 // M 33 .. 4096, N 512 .. 14336, K 512 .. 7168, 11 % rms.  The choice among those is 0.6 % slower than the best of each shape on
 // average (1.3 % with a scale per row of B), 1.6 % with the 8-bit integer products' figures.  With a scale per row the FMAs are
 // twice as many instructions, and the 256 x 256 tile's accumulators leave no registers for them (4096 x 4096 x 7168: 150 us, 128
@@ -84,7 +85,8 @@ inline bool fp8_tall_tiles(bool gated, int64_t rows, int64_t N, int64_t E, int c
   return mean > 24 && tiles > slots;
 }
 
-// Few rows: a scale per block of B, a bf16 result.
+// Few rows: a scale per block of B, a bf16 result.  That is what a token's projection is; fp8_rows has no other ending, and
+// binary32 results (weights' gradients) and scales by row (the same) come with many rows.
 inline bool fp8_on_rows(bool row_b, bool f32, int64_t M, int64_t N, int64_t K) {
   return !row_b && !f32 && fp8_rows_ok(M, N, K);
 }

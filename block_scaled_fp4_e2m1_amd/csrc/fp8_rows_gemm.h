@@ -203,6 +203,11 @@ inline hipError_t launch_fp8_rows(const Fp8Args& a, hipStream_t stream) {
 // Up to four rows in bf16, quantised inside: what fits in LDS, and where it is cheaper than a launch of its own.  us,
 // inside against two launches: 1 x 4096 x 7168 7.8, 10.1; 4 x 512 x 512 4.0, 4.9; 2 x 14336 x 4096 13.4, 15.2; but 3 x
 // 65536 x 1024 26.6, 21.8.
+//
+// Every workgroup of 16 columns quantises all M K values: what the launch saves is lost again when N is large, sooner with
+// more rows and later with longer sums, which the last bound follows by fit.  It keeps to the safe side: one row is faster
+// inside up to some N = 16384, 24576, 60000 of K 512, 1024, 2048 and past 131072 of 3584 (bound: 16384, 16384, 32768, 100352),
+// and calls just past it lose up to a third to it (2 x 10000 x 1024 inside 6.1, apart 8.1; 3 x 8192 x 512 4.6, 5.8).
 inline bool fp8_rows_quant_ok(int64_t M, int64_t N, int64_t K) {
   const int64_t lds = (M * fp8_blocks(K) * (kFp8Block + 4) + 15) / 16 * 16 + (2 * M * K + 1023) / 1024 * 1024;
   return M <= 4 && fp8_blocks(K) <= 512 && lds <= kFp8RowsQuantBytes &&

@@ -50,7 +50,8 @@ struct Rows<float> {
 // Sorted rows of 64 MiB or more are written and read without a place in the last-level cache (256 MiB for all tensors
 // of a step): a copy there only pushes others out.  There and back with gradients, bf16, us, without and with:
 // 5600 rows of 7168 (80 MB) 113, 99; 32768 553, 512; there and back only, 28000 rows of 4096 124, 99; but 8024 of 4096
-// (66 MB), which the next call finds in the cache, 33, 35.
+// (66 MB), which the next call finds in the cache, 33, 35.  The rows of sort_permute_few are written as any others: its 4096
+// pairs at most come to 64 MiB only in rows of 16 KiB and more.
 inline bool streamed(int64_t rows, int64_t row_bytes) { return rows * row_bytes >= (int64_t)64 << 20; }
 
 template <bool kStream>

@@ -573,7 +573,7 @@ BSFP4_API bsfp4_status bsfp4_block_norm_backward(const bsfp4_block_norm_args* ar
  *        zeros), st float [MB, K]; both or neither
  *
  * bsfp4_fp8_quantize_weight: the same with one scale per 128 x 128 block of each
- *   of E matrices (1 <= E <= 1024).
+ *   of E matrices (1 <= E <= 1024, E NB KB < 2^24).
  *   W    device bf16 [E, N, K], N > 0, K % 16 == 0, K < 2^22, N < 2^22
  *   q    device [E, N, K], s float [E, NB, KB]; both or neither
  *   qt   device [E, K, N16], st float [E, KB, NB]: the transposed weight, the
@@ -642,7 +642,7 @@ BSFP4_API bsfp4_status bsfp4_fp8_linear_backward(const uint16_t* dy, const uint1
  *   row (zeros for dropped pairs).
  *   topk_ids        device int32 [T, topk], any values
  *   x               device [T, row_bytes], or NULL: only the lists are written
- *   row_bytes       > 0, % 16 == 0 (any element type: rows are copied)
+ *   row_bytes       > 0, < 2^26, % 16 == 0 (any element type: rows are copied)
  *   xs              device [n, row_bytes] (with x)
  *   expert_offsets  device int32 [E+1]: expert e's rows are [off[e], off[e+1]),
  *                   dropped pairs' [off[E], n)
